@@ -193,10 +193,10 @@ def prepare(case, seed):
         n_own = _attend_inputs(st, c, g)
     if own:
         from kv_cache_compression_ua_b200 import ua
-        st["cache"] = ua.KV8Cache(B, Hkv, d, st["cap"], act, st["kc"], st["vc"], st["ks"], st["vs"], st["kt"], st["vt"],
+        st["cache"] = ua.KVQCache(B, Hkv, d, st["cap"], act, st["kc"], st["vc"], st["ks"], st["vs"], st["kt"], st["vt"],
                                   n_own, page_table=st["table"])
         if c["op"] == "attend":
-            st["ws"] = ua.alloc_workspace(ua.kv8_attend_workspace_size(st["cache"], H, T), "cuda")
+            st["ws"] = ua.alloc_workspace(ua.kvq_attend_workspace_size(st["cache"], H, T), "cuda")
     return st
 
 
@@ -340,12 +340,12 @@ def run(st):
             return ua.qk_norm_rope_bwd(st["q"], st["k"], st["wq"], st["wk"], st["dq"], st["dk"], pos=st["pos"], eps=EPS,
                                        theta=theta)
         if op == "append":
-            q = ua.kv8_append(st["cache"], st["k"], st["v"], st["q"], wq=st["wq"], wk=st["wk"], pos=st["pos"],
+            q = ua.kvq_append(st["cache"], st["k"], st["v"], st["q"], wq=st["wq"], wk=st["wk"], pos=st["pos"],
                               n_new=st["n_new"], start=st["start"], eps=EPS, theta=THETA)
             return {"q": q, "k": st["kc"], "v": st["vc"], "kscale": st["ks"], "vscale": st["vs"], "ktail": st["kt"],
                     "vtail": st["vt"], "n": st["cache"].n_kept}
         lse = torch.empty(c["B"], c["H"], c["T"], dtype=torch.float32, device="cuda")
-        o = ua.kv8_attend(st["cache"], st["q"], g=st["gate"], bias=st["bias"], lse=lse, ws=st["ws"])
+        o = ua.kvq_attend(st["cache"], st["q"], g=st["gate"], bias=st["bias"], lse=lse, ws=st["ws"])
         return {"o": o, "lse": lse}
     if op == "append":
         return _run_append(st)
