@@ -354,6 +354,124 @@ ua_status ua_decode_step_split(const ua_cache* cache, int H, const void* q, cons
                                uint32_t* evict_bits, int32_t* kept_idx, int flags, void* ws, size_t ws_bytes,
                                void* stream);
 
+/* ------------------------------------------------------------------ softmax layers
+ * The full-softmax attention layers that stand beside UA layers: every eighth layer of the hybrid
+ * UA-Softmax stacks (paperlayer.ai summary App. D, Table 5), and the baselines UA is compared with
+ * (normalised queries and keys, App. E Table 6; an output gate, §5).  Their cache is never pruned,
+ * so next to UA's self-pruning caches it is nearly all of the memory: it is held in 8 bits.
+ * Three operators: the norm of queries and keys with the position rotation (forward and
+ * backward, also usable in front of ua_prefill_fwd / ua_prefill_bwd with the rotation off), the
+ * append of new keys and values to the 8-bit cache, and attention over that cache.
+ *
+ * Shape of the queries and keys.  A token's heads are contiguous ([H][d]); q_ld, k_ld and v_ld
+ * are the elements from one token to the next of the INPUT tensors q, k and v (0: dense, H*d or
+ * Hkv*d), so that the three may be slices of one fused projection's output; sequence b starts
+ * T tokens after sequence b-1.  Strides are multiples of 16 bytes.  Outputs and gradients are
+ * dense.  Any H, Hkv >= 1; d 64 or 128. */
+typedef struct {
+    int B, T, H, Hkv, d;
+    long long q_ld, k_ld, v_ld;
+    float eps;            /* added to the mean square; finite, >= 0 */
+    double rope_theta;    /* RoPE base; 0: no rotation */
+    ua_dtype dtype;
+} ua_qk_shape;
+
+/* ------------------------------------------------------------------ norm and rotation
+ * Per head x of every token (w = wq for queries, wk for keys):
+ *   n = w (.) x * rstd,  rstd = 1/sqrt(mean(x^2) + eps)      (w == NULL: n = x, no norm)
+ *   y = R(pos) n   (pairs m, m + d/2, angle pos * theta^(-2m/d); rope_theta == 0: y = n)
+ * q, q_out [B,T,H,d] act; k, k_out [B,T,Hkv,d] act; wq, wk [d] f32 or NULL; pos [B,T] int32 or
+ * NULL (pos = t).  Either q and q_out or k and k_out may both be NULL (that side is left out).
+ * Sums, angles (double) and the rotation are held in 32 bits or more; one rounding at the end. */
+ua_status ua_qk_norm_rope_fwd(const ua_qk_shape* shape, const void* q, const void* k, const float* wq,
+                              const float* wk, const int32_t* pos, void* q_out, void* k_out, void* stream);
+
+/* Gradients of sum(dq_out * q_out) + sum(dk_out * k_out) with respect to q, k, wq and wk:
+ *   g = R(-pos) dy;  dw = sum g (.) x * rstd;  dx = rstd * (n' - xh * mean(n' (.) xh)),
+ *   n' = g (.) w, xh = x * rstd     (w == NULL: dx = g, and no dw)
+ * dq_out, dq [B,T,H,d] act, dk_out, dk [B,T,Hkv,d] act, dwq, dwk [d] f32 (summed over tokens and
+ * heads; required with wq / wk, ignored without).  rstd is formed again from x, nothing is saved
+ * by the forward.  No atomics: the result of one device model is the same in every run.  ws: scratch of
+ * ua_qk_norm_rope_bwd_workspace_size bytes (overwritten). */
+ua_status ua_qk_norm_rope_bwd_workspace_size(const ua_qk_shape* shape, size_t* bytes);
+ua_status ua_qk_norm_rope_bwd(const ua_qk_shape* shape, const void* q, const void* k, const float* wq,
+                              const float* wk, const int32_t* pos, const void* dq_out, const void* dk_out,
+                              void* dq, void* dk, float* dwq, float* dwk, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* ------------------------------------------------------------------ 8-bit cache
+ * Slot j of sequence b holds the rotated key and the value of its j-th token.  Slots come in
+ * blocks of 64 with one scale for each block and KV head, of keys and of values each:
+ *   UA_KVQ_INT8: s = amax/127, code = round(x/s);  UA_KVQ_E4M3: s = the smallest power of two
+ *   with amax/s <= 448, code = e4m3(x/s)           (round to nearest even; value = code * s;
+ *   a block whose amax is below 2^-100 has s = 0)
+ * A block is encoded once, when its 64th slot is filled, from rows kept until then in the
+ * activation type: the unfinished block and the one before it live in a ring of 128 rows per
+ * sequence and head (slot j in row j % 128).  What a finished block holds therefore does not
+ * depend on how its tokens were split into calls, and recent tokens are exact.  The unfinished
+ * block needs no page.
+ *   k, v            [pages, Hkv, page_size, d] codes, 8 bits each
+ *   k_scale, v_scale [pages, Hkv, page_size/64] f32
+ *   k_ring, v_ring  [B, Hkv, 128, d] act
+ *   n_kept [B] int32 slots filled;  ring_state [B+1] int32: per sequence the highest slot count
+ *   since its cache was last begun at 0, then a counter of the append that is zero between calls
+ *   (initialise: the values of n_kept, then 0)
+ * page_table == NULL: one page of `capacity` slots per sequence (page b; capacity a multiple of
+ * 64).  Otherwise slot j of sequence b lies in page page_table[b*max_pages + j/page_size], page_size a
+ * power of two, 128 <= page_size <= 2^20, capacity == max_pages*page_size.  Page ids are checked
+ * where they are used: one outside [0, pool_pages) raises UA_ERR_INVALID_ARG in the device status and its
+ * access is skipped.  capacity < 2^30.
+ * A key or value that is not finite makes its whole block's scale NaN when the block is encoded:
+ * every output row that sees a slot of that block is then NaN, and no other. */
+typedef enum { UA_KVQ_INT8 = 0, UA_KVQ_E4M3 = 1 } ua_kvq_format;
+
+typedef struct {
+    int B, Hkv, d, capacity;
+    ua_dtype dtype;       /* act: the ring, q, k, v, o */
+    ua_kvq_format format;
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    void* k_ring;
+    void* v_ring;
+    int32_t* n_kept;
+    int32_t* ring_state;
+    int page_size, max_pages, pool_pages;
+    const int32_t* page_table;
+} ua_kvq;
+
+/* Append T tokens (the first n_new[b] of sequence b; n_new [B] int32 or NULL: T) at slots start[b]
+ * .. (start [B] int32 or NULL: n_kept[b]), then n_kept[b] = start[b] + n_new[b].  Keys are normalised (wk
+ * != NULL) and rotated as in ua_qk_norm_rope_fwd on the way, with pos [B,T] int32 or NULL (the
+ * slot's number); values are stored as they are.  q != NULL: queries [B,T,H,d] are normalised and
+ * rotated likewise into q_out (all T rows, whatever n_new).  k, v [B,T,Hkv,d] act.
+ * start below n_kept takes tokens back (rejected drafts): it must lie on a block's first slot,
+ * or its block's earlier rows must still be in the ring: ring_state[b] <= 64*floor(start/64) + 128
+ * (always so for up to 64 tokens taken back from the highest slot count).  A start above n_kept, below 0 or without its rows, or n_new
+ * outside [0, T], raises UA_ERR_INVALID_ARG in the device status, a sequence that would pass the
+ * capacity UA_ERR_CAPACITY; that sequence is left as it was.  Calls on one cache must not overlap on the GPU. */
+ua_status ua_kvq_append(const ua_kvq* cache, const ua_qk_shape* shape, const void* q, const void* k,
+                        const void* v, const float* wq, const float* wk, const int32_t* pos,
+                        const int32_t* n_new, const int32_t* start, void* q_out, void* stream);
+
+/* Attention of Tq queries per sequence (the first n_q[b]; n_q [B] int32 or NULL: Tq) over its
+ * cache of n = n_kept[b] slots: query i is the token in slot n - n_q + i and sees the slots up to
+ * its own.  q [B,Tq,H,d] act is taken as it is (already rotated); head h reads KV head h/(H/Hkv).
+ *   x_ij = scale * q_i . k_j + bias_j;   o_i = sum_j softmax_j(x_ij) v_j  (.) sigmoid(g_i)
+ * bias [B,Hkv,capacity] f32 or NULL, added to the logits: -inf hides a slot (UA's frozen decay
+ * log-biases or FoX's forget gate; any finite value, the lowest too, only weighs).  g [B,Tq,H,d]
+ * act or NULL (no gate).  o [B,Tq,H,d] act; lse [B,H,Tq] f32 natural log or NULL.  A query that
+ * sees nothing gets o = 0, lse = -inf; rows i >= n_q[b] of o and lse are left as they were.
+ * Any Tq >= 1; made for single tokens and drafts (16 rows Tq*H/Hkv per pass over the cache).
+ * n_kept outside [0, capacity] or n_q outside [0, Tq] raises UA_ERR_INVALID_ARG in the device
+ * status and the sequence is taken as empty.  ws: as for ua_decode_step_split, zeroed once before its first use;
+ * its counters are zero again after every call; calls that share it must not overlap on the GPU. */
+ua_status ua_kvq_attend_workspace_size(const ua_kvq* cache, int H, int Tq, size_t* bytes);
+ua_status ua_kvq_attend(const ua_kvq* cache, int H, int Tq, const void* q, const void* g, const float* bias,
+                        const int32_t* n_q, float scale, void* o, float* lse, void* ws, size_t ws_bytes,
+                        void* stream);
+
 /* ------------------------------------------------------------------ status
  * Synchronises `stream`, returns the device status word accumulated since the last call
  * (0 = no error, else a ua_status code) in *code, and clears it. */

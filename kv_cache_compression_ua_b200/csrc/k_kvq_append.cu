@@ -1,0 +1,268 @@
+// k_kvq_append.cu -- append of keys and values to the 8-bit cache: per-head norm and position
+// rotation of the keys on the way, the ring of recent rows, and the encoding of every block of 64
+// slots that the call fills; the step's queries are normalised and rotated by further CTAs of
+// the same launch (formulas and layout in include/ua.h).
+//
+// Bound: HBM for prompts (each key and value read once in the activation type, written once in
+// 8 bits), launch latency for single tokens.  One CTA owns a block of 64 slots of hpc KV heads:
+// CH = DH/16 lanes a row, every element of the block in registers between the one read and the
+// write of its code, so the block's largest magnitude costs one reduction and no second read.
+// The thread's eight angles are formed once and serve all hpc heads.
+#include <cuda_fp8.h>
+
+#include "qk_norm.cuh"
+#include "ua_profile.h"
+
+namespace ua {
+
+namespace {
+
+struct SeqState {
+    int start, n_new;       // n_new = 0: nothing to append (or a refused sequence)
+    int refused;            // status to raise, 0: none
+};
+
+// What sequence b appends.  Refused: n_new or start out of range, earlier rows of the start's
+// block no longer in the ring, capacity.
+__device__ __forceinline__ SeqState seq_state(const KvqAppendParams& p, int b) {
+    SeqState s;
+    const int n0 = p.c.n_kept[b];
+    s.start = p.start ? p.start[b] : n0;
+    s.n_new = p.n_new ? p.n_new[b] : p.n.T;
+    s.refused = 0;
+    if (n0 < 0 || n0 > p.c.cap || s.n_new < 0 || s.n_new > p.n.T || s.start < 0 || s.start > n0)
+        s.refused = UA_ERR_INVALID_ARG;
+    else if (s.start % kKvqBlock != 0 && p.c.ring_state[b] > s.start / kKvqBlock * kKvqBlock + kKvqRing)
+        s.refused = UA_ERR_INVALID_ARG;
+    else if (s.n_new > p.c.cap - s.start)
+        s.refused = UA_ERR_CAPACITY;
+    if (s.refused) {
+        s.n_new = 0;
+        s.start = 0;
+    }
+    return s;
+}
+
+// Scale of a block from the bits of its largest magnitude, and the factor or divisor of the
+// encoding.  int8: s = amax / 127, x / s rounded.  e4m3: the format floats, so a power of two
+// loses nothing against amax / 448 and makes x / s exact: s = 2^(E - 8), or 2^(E - 7) where amax > 448 * 2^(E - 8)
+// (448 = 1.75 * 2^8), E the exponent of amax.
+template <bool E4M3> __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
+    if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);      // a value is not finite
+    if (amax_bits < 0x0d800000u) return 0.f;                                // below 2^-100
+    if constexpr (E4M3) {
+        const int e = (int)(amax_bits >> 23) - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+        return __uint_as_float((uint32_t)e << 23);
+    } else {
+        return __uint_as_float(amax_bits) / 127.f;
+    }
+}
+
+// 8 codes of a row's chunk
+template <bool E4M3> __device__ __forceinline__ uint2 encode8(const float* x, float s) {
+    uint32_t w[2] = {0, 0};
+    if (s > 0.f) {                                       // (not for 0 or NaN: codes 0)
+        if constexpr (E4M3) {
+            const float inv = 1.f / s;                   // a power of two: exact
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv),
+                                                             __NV_SATFINITE, __NV_E4M3);
+                w[i / 2] |= c2 << (16 * (i & 1));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = max(-127, min(127, __float2int_rn(x[i] / s)));
+                w[i / 4] |= (uint32_t)(c & 0xff) << (8 * (i & 3));
+            }
+        }
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// grid: B * (Hkv / hpc) * nb block CTAs, then q_tiles * q_split query CTAs; 4 * DH threads
+template <typename T, int DH, bool E4M3>
+__global__ void __launch_bounds__(4 * DH) k_kvq_append(KvqAppendParams p) {
+    constexpr int CH = DH / 16, HALF = DH / 2, NW = 4 * DH / 32;
+    __shared__ float s_cos[kNormTokens * HALF], s_sin[kNormTokens * HALF];
+    __shared__ double s_f[HALF];
+    __shared__ uint32_t s_max[2][2][NW];
+    __shared__ int s_last;
+    grid_dep_wait();
+    const int tid = threadIdx.x, T_ = p.n.T, Hkv = p.c.Hkv;
+    const int groups = Hkv / p.hpc, kv_ctas = p.c.B * groups * p.nb;
+    if ((int)blockIdx.x >= kv_ctas) {                    // queries
+        const int i = blockIdx.x - kv_ctas;
+        const long long n0 = (long long)(i / p.q_split) * kNormTokens;
+        float cs[8], sn[8];
+        if (p.n.rope) {
+            auto posf = [&](long long n) {
+                if (p.n.pos) return p.n.pos[n];
+                const int b = (int)(n / T_);
+                return (p.start ? p.start[b] : p.c.n_kept[b]) + (int)(n - (long long)b * T_);
+            };
+            tile_angles<DH>(s_cos, s_sin, n0, p.n.N, p.n.rf, s_f, posf, cs, sn);
+        }
+        QkNormParams q = p.n;
+        q.k = nullptr;
+        norm_rope_tile<T, DH>(q, n0, i % p.q_split, p.q_split, cs, sn);
+    } else {
+        const int j = blockIdx.x % p.nb, gi = (blockIdx.x / p.nb) % groups, b = blockIdx.x / p.nb / groups;
+        const int row = tid / CH, c = tid % CH;
+        const SeqState s = seq_state(p, b);
+        if (s.refused && j == 0 && gi == 0 && tid == 0) raise_status(s.refused);
+        const int end = s.start + s.n_new, j0 = s.start / kKvqBlock, jl = end / kKvqBlock;   // jl: unfinished block
+        const int mine = j0 + j;
+        if (s.n_new > 0 && mine * kKvqBlock < end) {
+            // Ring rows are kept for blocks jl - 1 and jl.  The first block may still need earlier
+            // rows out of the ring, from the places that the kept block of the same parity takes:
+            // that block's rows are then written by the first block's CTA, after it has read them.
+            const bool old_rows = s.start % kKvqBlock != 0 && (j0 + 1) * kKvqBlock <= end;
+            auto shares_first = [&](int blk) { return old_rows && blk > j0 && ((blk - j0) & 1) == 0; };
+            const int kept_here[2] = {mine >= jl - 1 && !shares_first(mine) ? mine : -1,
+                                      j == 0 ? (shares_first(jl) ? jl : shares_first(jl - 1) ? jl - 1 : -1) : -1};
+            if (tid < HALF) s_f[tid] = p.n.rf.f[tid];
+            __syncthreads();
+            int buf = 0;
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
+                const int blk = pass == 0 ? mine : kept_here[1];
+                if (blk < 0) continue;
+                const bool keep = pass == 1 || kept_here[0] >= 0;
+                const bool full = pass == 0 && (blk + 1) * kKvqBlock <= end;
+                const int slot = blk * kKvqBlock + row, t = slot - s.start;
+                const bool is_new = t >= 0 && slot < end, old = full && t < 0;
+                const long long n = (long long)b * T_ + t;
+                const long long crow = full ? kvq_row(p.c, b, blk) : -1;
+                float cs[8], sn[8];
+                if (p.n.rope && is_new) {
+                    const int pos = p.n.pos ? p.n.pos[n] : slot;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) rope_cs_pi(pos, s_f[8 * c + e], cs + e, sn + e);
+                }
+#pragma unroll 1
+                for (int hh = 0; hh < p.hpc; ++hh) {
+                    const int h = gi * p.hpc + hh;
+                    const size_t ring = (((size_t)b * Hkv + h) * kKvqRing + (slot & (kKvqRing - 1))) * DH + 8 * c;
+                    T* kr = static_cast<T*>(p.c.kr) + ring;
+                    T* vr = static_cast<T*>(p.c.vr) + ring;
+                    Raw8<T> ka, kb, va, vb;
+                    ka.zero(); kb.zero(); va.zero(); vb.zero();
+                    if (is_new) {
+                        const T* ks = static_cast<const T*>(p.n.k) + n * p.n.k_ld + (long long)h * DH + 8 * c;
+                        const T* vs = static_cast<const T*>(p.v) + n * p.v_ld + (long long)h * DH + 8 * c;
+                        ka.ld(ks); kb.ld(ks + HALF);
+                        va.ld(vs); vb.ld(vs + HALF);
+                    } else if (old) {
+                        ka.ld(kr); kb.ld(kr + HALF);
+                        va.ld(vr); vb.ld(vr + HALF);
+                    }
+                    float x0[8], x1[8];
+                    ka.get(x0);
+                    kb.get(x1);
+                    {
+                        float y0[8], y1[8], w0[8], w1[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) { y0[e] = x0[e]; y1[e] = x1[e]; }
+                        if (p.n.wk != nullptr) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                w0[e] = __ldg(p.n.wk + 8 * c + e);
+                                w1[e] = __ldg(p.n.wk + HALF + 8 * c + e);
+                            }
+                            norm_row<DH>(y0, y1, w0, w1, p.n.eps);
+                        }
+                        if (is_new) {
+                            if (p.n.rope) rotate_row(y0, y1, cs, sn);
+                            ka.put(y0);                  // the cache holds the activation type: codes are
+                            kb.put(y1);                  // formed from the rounded key, however it came
+                            ka.get(x0);
+                            kb.get(x1);
+                        }
+                    }
+                    if (full) {
+                        float z0[8], z1[8];
+                        va.get(z0);
+                        vb.get(z1);
+                        uint32_t mk = 0, mv = 0;         // non-negative floats order as their bits, NaN last
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            mk = max(mk, max(__float_as_uint(x0[e]) & 0x7fffffffu, __float_as_uint(x1[e]) & 0x7fffffffu));
+                            mv = max(mv, max(__float_as_uint(z0[e]) & 0x7fffffffu, __float_as_uint(z1[e]) & 0x7fffffffu));
+                        }
+                        mk = __reduce_max_sync(0xffffffffu, mk);
+                        mv = __reduce_max_sync(0xffffffffu, mv);
+                        if ((tid & 31) == 0) {
+                            s_max[buf][0][tid >> 5] = mk;
+                            s_max[buf][1][tid >> 5] = mv;
+                        }
+                        __syncthreads();                 // (also: every earlier row has been read from the ring)
+#pragma unroll
+                        for (int i = 0; i < NW; ++i) {
+                            mk = max(mk, s_max[buf][0][i]);
+                            mv = max(mv, s_max[buf][1][i]);
+                        }
+                        buf ^= 1;
+                        if (crow >= 0) {
+                            const long long r = crow + (long long)h * p.c.bpp;
+                            const float sk = block_scale<E4M3>(mk), sv = block_scale<E4M3>(mv);
+                            uint8_t* dk = p.c.k + r * (kKvqBlock * DH) + row * DH + 8 * c;
+                            uint8_t* dv = p.c.v + r * (kKvqBlock * DH) + row * DH + 8 * c;
+                            *reinterpret_cast<uint2*>(dk) = encode8<E4M3>(x0, sk);
+                            *reinterpret_cast<uint2*>(dk + HALF) = encode8<E4M3>(x1, sk);
+                            *reinterpret_cast<uint2*>(dv) = encode8<E4M3>(z0, sv);
+                            *reinterpret_cast<uint2*>(dv + HALF) = encode8<E4M3>(z1, sv);
+                            if (tid == 0) {
+                                p.c.ks[r] = sk;
+                                p.c.vs[r] = sv;
+                            }
+                        }
+                    }
+                    if (is_new && keep) {
+                        ka.st(kr); kb.st(kr + HALF);
+                        va.st(vr); vb.st(vr + HALF);
+                    }
+                }
+            }
+        }
+    }
+    // The last CTA to arrive sets the slot counts: all others have read them.
+    __syncthreads();
+    if (tid == 0) {
+        __threadfence();
+        const int at = atomicAdd(p.c.ring_state + p.c.B, 1);
+        if (at >= (int)gridDim.x) raise_status(UA_ERR_INVALID_ARG);         // the counter did not start at 0
+        s_last = at == (int)gridDim.x - 1;
+    }
+    __syncthreads();
+    if (s_last) {
+        for (int b = tid; b < p.c.B; b += blockDim.x) {
+            const SeqState s = seq_state(p, b);
+            if (s.refused) continue;
+            const int end = s.start + s.n_new;
+            p.c.n_kept[b] = end;
+            p.c.ring_state[b] = s.start == 0 ? end : max(p.c.ring_state[b], end);
+        }
+        if (tid == 0) p.c.ring_state[p.c.B] = 0;
+    }
+}
+
+template <typename T, int DH, bool E4M3> cudaError_t append(const KvqAppendParams& p, cudaStream_t s) {
+    const int ctas = p.c.B * (p.c.Hkv / p.hpc) * p.nb + p.q_tiles * p.q_split;
+    UA_PROFILE("k_kvq_append", s);
+    return launch_dependent(k_kvq_append<T, DH, E4M3>, dim3(ctas), dim3(4 * DH), 0, s, p);
+}
+
+template <typename T> cudaError_t append_t(const KvqAppendParams& p, int d, bool e4m3, cudaStream_t s) {
+    if (d == 64) return e4m3 ? append<T, 64, true>(p, s) : append<T, 64, false>(p, s);
+    return e4m3 ? append<T, 128, true>(p, s) : append<T, 128, false>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_kvq_append(const KvqAppendParams& p, int d, bool bf16, bool e4m3, cudaStream_t s) {
+    return bf16 ? append_t<__nv_bfloat16>(p, d, e4m3, s) : append_t<float>(p, d, e4m3, s);
+}
+
+}  // namespace ua

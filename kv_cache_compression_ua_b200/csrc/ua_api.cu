@@ -195,6 +195,106 @@ CacheView view(const ua_cache* c) {
     return v;
 }
 
+// ------------------------------------------------------------------ softmax layers
+ua_status check_qk(const ua_qk_shape* s) {
+    if (!s) return UA_ERR_INVALID_ARG;
+    if (s->B < 1 || s->T < 1 || s->H < 1 || s->Hkv < 1) return UA_ERR_INVALID_ARG;
+    if (!(s->rope_theta >= 0.0) || isinf(s->rope_theta) || !(s->eps >= 0.f) || isinf(s->eps)) return UA_ERR_INVALID_ARG;
+    if (s->d != 64 && s->d != 128) return UA_ERR_UNSUPPORTED;
+    if (s->dtype != UA_F32 && s->dtype != UA_BF16) return UA_ERR_UNSUPPORTED;
+    const long long heads[] = {s->H, s->Hkv, s->Hkv}, lds[] = {s->q_ld, s->k_ld, s->v_ld};
+    const int e = s->dtype == UA_BF16 ? 2 : 4;
+    for (int i = 0; i < 3; ++i) {
+        if (heads[i] * s->d > INT32_MAX) return UA_ERR_UNSUPPORTED;
+        if (lds[i] != 0 && lds[i] < heads[i] * s->d) return UA_ERR_INVALID_ARG;
+        if (lds[i] * e % 16 != 0) return UA_ERR_ALIGNMENT;
+    }
+    // one CTA takes 16 tokens
+    if ((long long)s->B * s->T > 16LL * INT32_MAX / 256) return UA_ERR_UNSUPPORTED;
+    return UA_OK;
+}
+
+QkNormParams qk_params(const ua_qk_shape* s, const void* q, const void* k, const float* wq, const float* wk,
+                       const int32_t* pos) {
+    QkNormParams p;
+    memset(&p, 0, sizeof(p));
+    p.N = (long long)s->B * s->T;
+    p.T = s->T; p.H = s->H; p.Hkv = s->Hkv;
+    p.q_ld = s->q_ld ? s->q_ld : (long long)s->H * s->d;
+    p.k_ld = s->k_ld ? s->k_ld : (long long)s->Hkv * s->d;
+    p.q = q; p.k = k; p.wq = wq; p.wk = wk; p.pos = pos;
+    p.eps = s->eps;
+    p.rope = s->rope_theta > 0.0;
+    if (p.rope) p.rf = rope_freq(s->rope_theta, s->d);
+    return p;
+}
+
+size_t qk_bwd_ws_bytes(const ua_qk_shape* s) {
+    const long long tiles = ((long long)s->B * s->T + 15) / 16;
+    return (size_t)std::min<long long>(tiles, kQkNormBwdCtas) * 2 * s->d * 4;
+}
+
+ua_status check_kvq(const ua_kvq* c) {
+    if (!c) return UA_ERR_INVALID_ARG;
+    if (c->B < 1 || c->Hkv < 1 || c->capacity < 1 || c->capacity >= (1 << 30)) return UA_ERR_INVALID_ARG;
+    if (c->d != 64 && c->d != 128) return UA_ERR_UNSUPPORTED;
+    if (c->dtype != UA_F32 && c->dtype != UA_BF16) return UA_ERR_UNSUPPORTED;
+    if (c->format != UA_KVQ_INT8 && c->format != UA_KVQ_E4M3) return UA_ERR_UNSUPPORTED;
+    if ((long long)c->Hkv * c->d > INT32_MAX || (long long)c->B * c->Hkv > INT32_MAX / 1024) return UA_ERR_UNSUPPORTED;
+    const void* ps[] = {c->k, c->v, c->k_scale, c->v_scale, c->k_ring, c->v_ring, c->n_kept, c->ring_state};
+    for (const void* p : ps)
+        if (!p) return UA_ERR_INVALID_ARG;
+    for (const void* p : ps)
+        if (!aligned(p, 16)) return UA_ERR_ALIGNMENT;
+    if (c->page_table) {
+        const int sz = c->page_size;
+        if (sz < 128 || sz > kMaxCapacity || (sz & (sz - 1)) != 0) return UA_ERR_INVALID_ARG;
+        if (c->max_pages < 1 || c->pool_pages < 1) return UA_ERR_INVALID_ARG;
+        if ((long long)c->max_pages * sz != c->capacity) return UA_ERR_INVALID_ARG;
+        if (!aligned(c->page_table, 4)) return UA_ERR_ALIGNMENT;
+    } else if (c->capacity % kKvqBlock != 0) {
+        return UA_ERR_INVALID_ARG;
+    }
+    return UA_OK;
+}
+
+KvqView kvq_view(const ua_kvq* c) {
+    KvqView v;
+    memset(&v, 0, sizeof(v));
+    v.B = c->B; v.Hkv = c->Hkv; v.cap = c->capacity;
+    v.k = static_cast<uint8_t*>(c->k); v.v = static_cast<uint8_t*>(c->v);
+    v.ks = c->k_scale; v.vs = c->v_scale; v.kr = c->k_ring; v.vr = c->v_ring;
+    v.n_kept = c->n_kept; v.ring_state = c->ring_state;
+    v.pt = c->page_table;
+    v.bpp = (c->page_table ? c->page_size : c->capacity) / kKvqBlock;
+    if (c->page_table) {
+        while ((1 << v.bpp_shift) < v.bpp) ++v.bpp_shift;
+        v.max_pages = c->max_pages;
+        v.pool_pages = c->pool_pages;
+    }
+    return v;
+}
+
+int kvq_row_tiles(const ua_kvq* c, int H, int Tq) {
+    const int rows = Tq * (H / c->Hkv), R = kvq_row_tile(rows);
+    return (rows + R - 1) / R;
+}
+
+size_t kvq_ws_counters(const ua_kvq* c, int H, int Tq) {
+    return round_up((size_t)c->B * c->Hkv * kvq_row_tiles(c, H, Tq) * 4, 256);
+}
+
+size_t kvq_ws_bytes(const ua_kvq* c, int H, int Tq) {
+    const int R = kvq_row_tile(Tq * (H / c->Hkv));
+    return kvq_ws_counters(c, H, Tq) + (size_t)kKvqAttendCtas * 2 * R * (c->d + 2) * 4;
+}
+
+ua_status check_kvq_heads(const ua_kvq* c, int H, int Tq) {
+    if (H < 1 || H % c->Hkv != 0 || Tq < 1) return UA_ERR_INVALID_ARG;
+    if ((long long)H * c->d > INT32_MAX || (long long)Tq * (H / c->Hkv) > INT32_MAX / 2) return UA_ERR_UNSUPPORTED;
+    return UA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -835,6 +935,129 @@ ua_status ua_prefill_fixed_rows(const ua_shape* s, const void* ws, size_t ws_byt
     if (e != cudaSuccess) return UA_ERR_CUDA;
     *rows = host;
     return UA_OK;
+}
+
+ua_status ua_qk_norm_rope_fwd(const ua_qk_shape* s, const void* q, const void* k, const float* wq, const float* wk,
+                              const int32_t* pos, void* q_out, void* k_out, void* stream) {
+    ua_status st = check_qk(s);
+    if (st != UA_OK) return st;
+    if ((!q && !k) || (!q != !q_out) || (!k != !k_out)) return UA_ERR_INVALID_ARG;
+    const void* ps[] = {q, k, q_out, k_out};
+    for (const void* x : ps)
+        if (x && !aligned(x, 16)) return UA_ERR_ALIGNMENT;
+    const void* ws4[] = {wq, wk, pos};
+    for (const void* x : ws4)
+        if (x && !aligned(x, 4)) return UA_ERR_ALIGNMENT;
+    QkNormParams p = qk_params(s, q, k, wq, wk, pos);
+    p.q_out = q_out; p.k_out = k_out;
+    return cuda_status(launch_qk_norm_fwd(p, s->d, s->dtype == UA_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+ua_status ua_qk_norm_rope_bwd_workspace_size(const ua_qk_shape* s, size_t* bytes) {
+    ua_status st = check_qk(s);
+    if (st != UA_OK) return st;
+    if (!bytes) return UA_ERR_INVALID_ARG;
+    *bytes = qk_bwd_ws_bytes(s);
+    return UA_OK;
+}
+
+ua_status ua_qk_norm_rope_bwd(const ua_qk_shape* s, const void* q, const void* k, const float* wq, const float* wk,
+                              const int32_t* pos, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                              float* dwq, float* dwk, void* ws, size_t ws_bytes, void* stream) {
+    ua_status st = check_qk(s);
+    if (st != UA_OK) return st;
+    if ((!q && !k) || !ws) return UA_ERR_INVALID_ARG;
+    if (q ? (!dq_out || !dq || (wq && !dwq)) : (dq_out || dq)) return UA_ERR_INVALID_ARG;
+    if (k ? (!dk_out || !dk || (wk && !dwk)) : (dk_out || dk)) return UA_ERR_INVALID_ARG;
+    const void* ps[] = {q, k, dq_out, dk_out, dq, dk};
+    for (const void* x : ps)
+        if (x && !aligned(x, 16)) return UA_ERR_ALIGNMENT;
+    const void* ws4[] = {wq, wk, pos, dwq, dwk};
+    for (const void* x : ws4)
+        if (x && !aligned(x, 4)) return UA_ERR_ALIGNMENT;
+    if (!aligned(ws, 256)) return UA_ERR_ALIGNMENT;
+    if (ws_bytes < qk_bwd_ws_bytes(s)) return UA_ERR_WORKSPACE;
+    QkNormParams p = qk_params(s, q, k, wq, wk, pos);
+    p.dq_out = dq_out; p.dk_out = dk_out; p.dq = dq; p.dk = dk; p.dwq = dwq; p.dwk = dwk;
+    p.part = static_cast<float*>(ws);
+    return cuda_status(launch_qk_norm_bwd(p, s->d, s->dtype == UA_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+ua_status ua_kvq_append(const ua_kvq* c, const ua_qk_shape* s, const void* q, const void* k, const void* v,
+                        const float* wq, const float* wk, const int32_t* pos, const int32_t* n_new,
+                        const int32_t* start, void* q_out, void* stream) {
+    ua_status st = check_kvq(c);
+    if (st != UA_OK) return st;
+    if ((st = check_qk(s)) != UA_OK) return st;
+    if (s->B != c->B || s->Hkv != c->Hkv || s->d != c->d || s->dtype != c->dtype) return UA_ERR_INVALID_ARG;
+    if (!k || !v || (!q != !q_out)) return UA_ERR_INVALID_ARG;
+    const void* ps[] = {q, k, v, q_out};
+    for (const void* x : ps)
+        if (x && !aligned(x, 16)) return UA_ERR_ALIGNMENT;
+    const void* ws4[] = {wq, wk, pos, n_new, start};
+    for (const void* x : ws4)
+        if (x && !aligned(x, 4)) return UA_ERR_ALIGNMENT;
+    KvqAppendParams p;
+    memset(&p, 0, sizeof(p));
+    p.c = kvq_view(c);
+    p.n = qk_params(s, q, k, wq, wk, pos);
+    p.n.q_out = q_out;
+    p.v = v;
+    p.v_ld = s->v_ld ? s->v_ld : (long long)s->Hkv * s->d;
+    p.n_new = n_new; p.start = start;
+    p.nb = (int)(((long long)s->T + 2 * kKvqBlock - 2) / kKvqBlock);
+    // all KV heads in one CTA share a token's angles; fewer heads a CTA where the blocks alone do
+    // not fill the GPU
+    p.hpc = s->Hkv;
+    while (p.hpc > 1 && (long long)s->B * p.nb * (s->Hkv / p.hpc) < 2 * 148) {
+        int next = p.hpc - 1;
+        while (s->Hkv % next) --next;
+        p.hpc = next;
+    }
+    if (q) {
+        p.q_tiles = (int)((p.n.N + 15) / 16);
+        const int quads = (s->H + 3) / 4;
+        p.q_split = p.q_tiles >= 148 ? 1 : std::min(quads, std::max(1, 148 / p.q_tiles));
+    }
+    if ((long long)s->B * (s->Hkv / p.hpc) * p.nb + (long long)p.q_tiles * p.q_split > INT32_MAX)
+        return UA_ERR_UNSUPPORTED;
+    return cuda_status(launch_kvq_append(p, s->d, s->dtype == UA_BF16, c->format == UA_KVQ_E4M3,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+ua_status ua_kvq_attend_workspace_size(const ua_kvq* c, int H, int Tq, size_t* bytes) {
+    ua_status st = check_kvq(c);
+    if (st != UA_OK) return st;
+    if ((st = check_kvq_heads(c, H, Tq)) != UA_OK) return st;
+    if (!bytes) return UA_ERR_INVALID_ARG;
+    *bytes = kvq_ws_bytes(c, H, Tq);
+    return UA_OK;
+}
+
+ua_status ua_kvq_attend(const ua_kvq* c, int H, int Tq, const void* q, const void* g, const float* bias,
+                        const int32_t* n_q, float scale, void* o, float* lse, void* ws, size_t ws_bytes,
+                        void* stream) {
+    ua_status st = check_kvq(c);
+    if (st != UA_OK) return st;
+    if ((st = check_kvq_heads(c, H, Tq)) != UA_OK) return st;
+    if (!q || !o || !ws || !isfinite(scale)) return UA_ERR_INVALID_ARG;
+    const void* ps[] = {q, g, o};
+    for (const void* x : ps)
+        if (x && !aligned(x, 16)) return UA_ERR_ALIGNMENT;
+    const void* ws4[] = {bias, n_q, lse};
+    for (const void* x : ws4)
+        if (x && !aligned(x, 4)) return UA_ERR_ALIGNMENT;
+    if (!aligned(ws, 256)) return UA_ERR_ALIGNMENT;
+    if (ws_bytes < kvq_ws_bytes(c, H, Tq)) return UA_ERR_WORKSPACE;
+    KvqAttendParams p;
+    memset(&p, 0, sizeof(p));
+    p.c = kvq_view(c);
+    p.H = H; p.G = H / c->Hkv; p.Tq = Tq; p.RT = kvq_row_tiles(c, H, Tq);
+    p.scale = scale; p.q = q; p.g = g; p.bias = bias; p.n_q = n_q; p.o = o; p.lse = lse;
+    p.cnt = static_cast<unsigned*>(ws);
+    p.part = reinterpret_cast<float*>(at(ws, kvq_ws_counters(c, H, Tq)));
+    return cuda_status(launch_kvq_attend(p, c->d, c->dtype == UA_BF16, c->format == UA_KVQ_E4M3,
+                                         static_cast<cudaStream_t>(stream)));
 }
 
 ua_status ua_set_wait_limit_ns(unsigned long long ns) {

@@ -337,6 +337,97 @@ cudaError_t launch_fwd_tc(const FwdTcLaunch& L, cudaStream_t s);
 // pincl [B*Hkv][nqt][Tpk]
 cudaError_t launch_fwd_tc128(const FwdTcLaunch& L, cudaStream_t s);
 
+// ------------------------------------------------------------------ softmax layers
+// Norm of queries and keys with the position rotation (k_qk_norm.cu).  Tokens are flattened,
+// N = B * T; a NULL q or k side is left out.
+struct QkNormParams {
+    long long N;
+    int T, H, Hkv;
+    long long q_ld, k_ld;          // elements between tokens of q and k
+    const void* q;
+    const void* k;
+    const float* wq;               // [d] or NULL: no norm
+    const float* wk;
+    const int32_t* pos;            // [N] or NULL: t
+    void* q_out;
+    void* k_out;
+    // backward
+    const void* dq_out;
+    const void* dk_out;
+    void* dq;
+    void* dk;
+    float* dwq;
+    float* dwk;
+    float* part;                   // [CTAs][2][d] partial gain gradients
+    float eps;
+    int rope;
+    RopeFreq rf;
+};
+constexpr int kQkNormBwdCtas = 148 * 4;   // most CTAs of the backward (rows of `part`)
+cudaError_t launch_qk_norm_fwd(const QkNormParams& p, int d, bool bf16, cudaStream_t s);
+cudaError_t launch_qk_norm_bwd(const QkNormParams& p, int d, bool bf16, cudaStream_t s);
+
+// 8-bit cache (see ua_kvq).
+constexpr int kKvqBlock = 64, kKvqRing = 128;
+struct KvqView {
+    int B, Hkv, cap;
+    uint8_t* k;
+    uint8_t* v;
+    float* ks;
+    float* vs;
+    void* kr;
+    void* vr;
+    int32_t* n_kept;
+    int32_t* ring_state;
+    const int32_t* pt;             // or NULL: page b
+    int bpp;                       // blocks per page
+    int bpp_shift;                 // log2(bpp) when paged
+    int max_pages, pool_pages;
+};
+
+// Row (of 64 slots: codes at row * 64 * d, scale at row) of block blk of sequence b, head 0;
+// head h is bpp rows further each.  -1: a page id outside the pool (status raised).
+__device__ __forceinline__ long long kvq_row(const KvqView& c, int b, int blk) {
+    if (c.pt == nullptr) return (long long)b * c.Hkv * c.bpp + blk;
+    const int pg = __ldg(c.pt + (size_t)b * c.max_pages + (blk >> c.bpp_shift));
+    if ((unsigned)pg >= (unsigned)c.pool_pages) {
+        raise_status(UA_ERR_INVALID_ARG);
+        return -1;
+    }
+    return (long long)pg * c.Hkv * c.bpp + (blk & (c.bpp - 1));
+}
+
+struct KvqAppendParams {
+    KvqView c;
+    QkNormParams n;                // q, k, gains, positions; n.pos NULL: the slot's number
+    const void* v;
+    long long v_ld;
+    const int32_t* n_new;          // or NULL: T
+    const int32_t* start;          // or NULL: n_kept
+    int nb;                        // blocks a sequence's tokens can touch
+    int hpc;                       // KV heads per CTA
+    int q_tiles, q_split;          // CTAs for the queries: token tiles x head splits
+};
+cudaError_t launch_kvq_append(const KvqAppendParams& p, int d, bool bf16, bool e4m3, cudaStream_t s);
+
+struct KvqAttendParams {
+    KvqView c;
+    int H, G, Tq;
+    int RT;                        // row tiles (of 8 or 16 rows Tq * G) per unit
+    float scale;
+    const void* q;
+    const void* g;
+    const float* bias;
+    const int32_t* n_q;
+    void* o;
+    float* lse;
+    unsigned* cnt;                 // [B * Hkv * RT] arrivals, zero between calls
+    float* part;                   // [CTAs][2][rows][d + 2] partial states
+};
+constexpr int kKvqAttendCtas = 148 * 3;   // most CTAs of the attention (slots of `part`)
+inline int kvq_row_tile(int rows) { return rows <= 8 ? 8 : 16; }
+cudaError_t launch_kvq_attend(const KvqAttendParams& p, int d, bool bf16, bool e4m3, cudaStream_t s);
+
 cudaError_t launch_prep(const PrepParams& p, bool bf16_in, bool bf16_work, cudaStream_t s);
 cudaError_t launch_boundary_simt(const BoundaryParams& p, cudaStream_t s);
 cudaError_t launch_fwd_simt(const FwdParams& p, bool bf16_act, cudaStream_t s);

@@ -49,12 +49,33 @@ class ua_cache(ctypes.Structure):
                 ("max_pages", ctypes.c_int), ("pool_pages", ctypes.c_int), ("page_table", ctypes.c_void_p)]
 
 
+class ua_qk_shape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("d", ctypes.c_int), ("q_ld", ctypes.c_longlong), ("k_ld", ctypes.c_longlong),
+                ("v_ld", ctypes.c_longlong), ("eps", ctypes.c_float), ("rope_theta", ctypes.c_double),
+                ("dtype", ctypes.c_int)]
+
+
+UA_KVQ_INT8, UA_KVQ_E4M3 = 0, 1
+KVQ_BLOCK, KVQ_RING = 64, 128   # slots that share a scale; recent rows kept in the activation type
+
+
+class ua_kvq(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("capacity", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("format", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("k_ring", ctypes.c_void_p),
+                ("v_ring", ctypes.c_void_p), ("n_kept", ctypes.c_void_p), ("ring_state", ctypes.c_void_p),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("pool_pages", ctypes.c_int),
+                ("page_table", ctypes.c_void_p)]
+
+
 EXPORTS = ("ua_prefill_workspace_size", "ua_prefill_fwd", "ua_prefill_bwd_workspace_size", "ua_prefill_bwd",
            "ua_cache_fill", "ua_cache_compact", "ua_decode_step", "ua_get_device_status",
            "ua_profile_enable", "ua_profile_reset", "ua_profile_read", "ua_status_string", "ua_version",
            "ua_prefill_fwd_noalloc", "ua_prefill_noalloc_max_scratch", "ua_prefill_tile_stats",
            "ua_set_wait_limit_ns", "ua_decode_workspace_size", "ua_decode_step_split", "ua_prefill_fixed_rows",
-           "ua_prefill_bwd_band_stats")
+           "ua_prefill_bwd_band_stats", "ua_qk_norm_rope_fwd", "ua_qk_norm_rope_bwd_workspace_size",
+           "ua_qk_norm_rope_bwd", "ua_kvq_append", "ua_kvq_attend_workspace_size", "ua_kvq_attend")
 
 
 class ua_kernel_time(ctypes.Structure):
@@ -97,6 +118,13 @@ def load_library(path: str = LIB_PATH):
     lib.ua_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
     lib.ua_decode_workspace_size.argtypes = [CP, I, ctypes.POINTER(S)]
     lib.ua_decode_step_split.argtypes = [CP, I] + [P] * 8 + [I, F, F, D, P, P, P, I, P, S, P]
+    QP, KP = ctypes.POINTER(ua_qk_shape), ctypes.POINTER(ua_kvq)
+    lib.ua_qk_norm_rope_fwd.argtypes = [QP] + [P] * 8
+    lib.ua_qk_norm_rope_bwd_workspace_size.argtypes = [QP, ctypes.POINTER(S)]
+    lib.ua_qk_norm_rope_bwd.argtypes = [QP] + [P] * 12 + [S, P]
+    lib.ua_kvq_append.argtypes = [KP, QP] + [P] * 10
+    lib.ua_kvq_attend_workspace_size.argtypes = [KP, I, I, ctypes.POINTER(S)]
+    lib.ua_kvq_attend.argtypes = [KP, I, I] + [P] * 4 + [F, P, P, P, S, P]
     lib.ua_status_string.argtypes = [I]
     lib.ua_status_string.restype = ctypes.c_char_p
     lib.ua_version.argtypes = []
@@ -561,6 +589,288 @@ def decode_step(cache: Cache, q, k, v, g, a_q, a_k, alpha, beta, pos_t: int, p: 
                                            float(theta), _ptr(o), _ptr(evict_bits), _ptr(kept_idx), flags,
                                            _stream(stream))
     _check("ua_decode_step", rc)
+    return o
+
+
+# ------------------------------------------------------------------ softmax layers
+def _heads(name, t, B, T, d, dtype, dev):
+    """Checks an input [B, T, heads, d] whose tokens' heads are contiguous (a dense tensor, or a slice
+    of a fused projection's output) and returns (heads, elements between tokens)."""
+    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != T or t.shape[3] != d:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{B}, {T}, heads, {d}]")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, the call runs on {dev}")
+    if not t.is_cuda:
+        raise ValueError("libua takes CUDA tensors")
+    n = t.shape[2]
+    if t.is_contiguous():
+        return n, n * d
+    sb, st, sh, se = t.stride()
+    ld = st if T > 1 else (sb if B > 1 else n * d)
+    if se != 1 or (n > 1 and sh != d) or (B > 1 and sb != T * ld) or ld < n * d:
+        raise ValueError(f"{name}: strides {t.stride()}, a token's heads must be contiguous and the tokens evenly spaced")
+    return n, ld
+
+
+def _dense(name, t, shape, dtypes, dev):
+    """Checks an output or side input of exactly this shape, dense."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {list(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, the call runs on {dev}")
+    if not t.is_contiguous():
+        raise ValueError("libua takes contiguous tensors")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+
+
+def _qk_shape(q, k, wq, wk, pos, eps, theta, v=None):
+    """(shape, device) of a norm / append call from its checked inputs (q or k may be None)."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q and k: at least one of them is needed")
+    if x.dim() != 4:
+        raise ValueError(f"q or k: shape {tuple(x.shape)}, expected [B, T, heads, d]")
+    B, T, _, d = x.shape
+    dev = x.device
+    H, q_ld = _heads("q", q, B, T, d, x.dtype, dev) if q is not None else (1, 0)
+    Hkv, k_ld = _heads("k", k, B, T, d, x.dtype, dev) if k is not None else (1, 0)
+    v_ld = 0
+    if v is not None:
+        hv, v_ld = _heads("v", v, B, T, d, x.dtype, dev)
+        if hv != Hkv:
+            raise ValueError(f"v: {hv} heads, expected {Hkv}")
+    _dense("wq", wq, (d,), F32, dev)
+    _dense("wk", wk, (d,), F32, dev)
+    _dense("pos", pos, (B, T), (torch.int32,), dev)
+    return ua_qk_shape(B, T, H, Hkv, d, q_ld, k_ld, v_ld, float(eps), float(theta or 0.0), _dtype_code(x.dtype)), dev
+
+
+def qk_norm_rope_fwd(q, k, wq=None, wk=None, *, pos=None, eps=1e-6, theta=500000.0, q_out=None, k_out=None,
+                     stream=None):
+    """ua_qk_norm_rope_fwd: RMS norm of every head with the gains wq, wk [d] (None: no norm on that
+    side) and the position rotation (theta 0: none), q [B,T,H,d] and k [B,T,Hkv,d] in one pass.  Either may
+    be None; both may be slices of a fused projection's output.  Returns dict(q, k)."""
+    shape, dev = _qk_shape(q, k, wq, wk, pos, eps, theta)
+    for name, x, y in (("q_out", q, q_out), ("k_out", k, k_out)):
+        if y is not None and x is None:
+            raise ValueError(f"{name}: given without its input")
+        if x is not None:
+            _dense(name, y, x.shape, (x.dtype,), dev)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    with torch.cuda.device(dev):
+        _check("ua_qk_norm_rope_fwd", load_library().ua_qk_norm_rope_fwd(
+            ctypes.byref(shape), _addr(q), _addr(k), _addr(wq), _addr(wk), _addr(pos), _addr(q_out), _addr(k_out),
+            _raw_stream(stream, dev)))
+    return {"q": q_out, "k": k_out}
+
+
+def qk_norm_rope_bwd_workspace_size(shape: ua_qk_shape) -> int:
+    n = ctypes.c_size_t(0)
+    _check("ua_qk_norm_rope_bwd_workspace_size",
+           load_library().ua_qk_norm_rope_bwd_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, *, pos=None, eps=1e-6, theta=500000.0, ws=None, stream=None):
+    """ua_qk_norm_rope_bwd: gradients of the forward with the same arguments.  Returns dict(dq, dk,
+    dwq, dwk), None for what the forward did not have."""
+    shape, dev = _qk_shape(q, k, wq, wk, pos, eps, theta)
+    for name, x, y in (("dq_out", q, dq_out), ("dk_out", k, dk_out)):
+        if (x is None) != (y is None):
+            raise ValueError(f"{name}: needed with its input, and only with it")
+        if x is not None:
+            _dense(name, y, x.shape, (x.dtype,), dev)
+    need = qk_norm_rope_bwd_workspace_size(shape)
+    if ws is None or _nbytes(ws) < need:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous tensor on the call's device is needed")
+    like = lambda x: None if x is None else torch.empty(x.shape, dtype=x.dtype, device=dev)  # noqa: E731
+    gr = {"dq": like(q), "dk": like(k), "dwq": like(wq) if q is not None else None,
+          "dwk": like(wk) if k is not None else None}
+    with torch.cuda.device(dev):
+        _check("ua_qk_norm_rope_bwd", load_library().ua_qk_norm_rope_bwd(
+            ctypes.byref(shape), _addr(q), _addr(k), _addr(wq), _addr(wk), _addr(pos), _addr(dq_out), _addr(dk_out),
+            _addr(gr["dq"]), _addr(gr["dk"]), _addr(gr["dwq"]), _addr(gr["dwk"]), ws.data_ptr(), _nbytes(ws),
+            _raw_stream(stream, dev)))
+    return gr
+
+
+KVQ_FORMATS = {torch.int8: UA_KVQ_INT8, torch.float8_e4m3fn: UA_KVQ_E4M3}
+
+
+@dataclass(frozen=True, eq=False)
+class KVQCache:
+    """Device tensors of one 8-bit cache of a softmax layer (see ua_kvq in ua.h).  k, v: codes [pages, Hkv,
+    page_size, d] (torch.int8 or torch.float8_e4m3fn), k_scale, v_scale [pages, Hkv, page_size/64],
+    k_ring, v_ring [B, Hkv, 128, d] in the activation type `dtype`, n_kept [B].  Without a page_table [B, max_pages]
+    sequence b is page b.  The tensors are checked once, here, and must stay the ones given."""
+    B: int
+    Hkv: int
+    d: int
+    capacity: int
+    dtype: torch.dtype
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    k_ring: torch.Tensor
+    v_ring: torch.Tensor
+    n_kept: torch.Tensor
+    ring_state: torch.Tensor | None = None      # None: as after an append up to n_kept
+    page_table: torch.Tensor | None = None
+
+    def __post_init__(self):
+        if self.k.dtype not in KVQ_FORMATS:
+            raise ValueError(f"cache.k: dtype {self.k.dtype}, expected {' or '.join(str(t) for t in KVQ_FORMATS)}")
+        if self.k.dim() != 4:
+            raise ValueError(f"cache.k: shape {tuple(self.k.shape)}, expected [pages, Hkv, page_size, d]")
+        if not self.k.is_cuda:
+            raise ValueError("libua takes CUDA tensors")
+        pages, ps = self.k.shape[0], self.k.shape[2]
+        dev = self.k.device
+        if self.ring_state is None:
+            object.__setattr__(self, "ring_state", torch.cat([self.n_kept.to(torch.int32),
+                                                              self.n_kept.new_zeros(1, dtype=torch.int32)]))
+        codes, scales = (pages, self.Hkv, ps, self.d), (pages, self.Hkv, ps // KVQ_BLOCK)
+        ring = (self.B, self.Hkv, KVQ_RING, self.d)
+        for name, shape, dt in (("k", codes, self.k.dtype), ("v", codes, self.k.dtype), ("k_scale", scales, torch.float32),
+                                ("v_scale", scales, torch.float32), ("k_ring", ring, self.dtype),
+                                ("v_ring", ring, self.dtype), ("n_kept", (self.B,), torch.int32),
+                                ("ring_state", (self.B + 1,), torch.int32)):
+            _dense(f"cache.{name}", getattr(self, name), shape, (dt,), dev)
+        max_pages = 0
+        if self.page_table is None:
+            if pages != self.B or self.capacity != ps or ps % KVQ_BLOCK:
+                raise ValueError(f"cache: {pages} pages of {ps} slots, expected {self.B} of {self.capacity}, a multiple of {KVQ_BLOCK}")
+        else:
+            max_pages = self.capacity // ps
+            if ps < 128 or ps & (ps - 1) or max_pages * ps != self.capacity:
+                raise ValueError(f"page_size {ps} must be a power of two >= 128 that divides the capacity {self.capacity}")
+            _dense("cache.page_table", self.page_table, (self.B, max_pages), (torch.int32,), dev)
+        paged = self.page_table is not None
+        object.__setattr__(self, "_struct", ua_kvq(
+            self.B, self.Hkv, self.d, self.capacity, _dtype_code(self.dtype), KVQ_FORMATS[self.k.dtype],
+            *[t.data_ptr() for t in (self.k, self.v, self.k_scale, self.v_scale, self.k_ring, self.v_ring, self.n_kept,
+                                     self.ring_state)],
+            ps if paged else 0, max_pages, pages if paged else 0, self.page_table.data_ptr() if paged else None))
+
+    @staticmethod
+    def _tensors(B, Hkv, d, pages, page_size, dtype, fmt, device):
+        kw = dict(device=device)
+        codes = lambda: torch.zeros(pages, Hkv, page_size, d, dtype=torch.uint8, **kw).view(fmt)  # noqa: E731
+        scales = lambda: torch.zeros(pages, Hkv, page_size // KVQ_BLOCK, dtype=torch.float32, **kw)  # noqa: E731
+        ring = lambda: torch.zeros(B, Hkv, KVQ_RING, d, dtype=dtype, **kw)  # noqa: E731
+        return (codes(), codes(), scales(), scales(), ring(), ring(), torch.zeros(B, dtype=torch.int32, **kw))
+
+    @staticmethod
+    def empty(B, Hkv, d, capacity, fmt=torch.float8_e4m3fn, dtype=torch.bfloat16, device="cuda"):
+        """Contiguous storage; the capacity is rounded up to whole blocks of 64 slots."""
+        capacity = -(-capacity // KVQ_BLOCK) * KVQ_BLOCK
+        return KVQCache(B, Hkv, d, capacity, dtype, *KVQCache._tensors(B, Hkv, d, B, capacity, dtype, fmt, device))
+
+    @staticmethod
+    def paged(B, Hkv, d, page_size, max_pages, pool_pages, fmt=torch.float8_e4m3fn, dtype=torch.bfloat16, device="cuda"):
+        """A pool of pool_pages pages of page_size slots (of all KV heads); every sequence may grow to
+        max_pages pages.  The page table starts empty (-1): give the sequences pages with a PagePool."""
+        table = torch.full((B, max_pages), -1, dtype=torch.int32, device=device)
+        return KVQCache(B, Hkv, d, max_pages * page_size, dtype,
+                        *KVQCache._tensors(B, Hkv, d, pool_pages, page_size, dtype, fmt, device), page_table=table)
+
+    @property
+    def page_size(self) -> int:
+        return self.k.shape[2]
+
+    @property
+    def pool_pages(self) -> int:
+        return self.k.shape[0]
+
+    def nbytes_per_entry(self) -> float:
+        """Bytes of one slot and KV head: two rows of codes and its share of the scales."""
+        return 2 * self.d + 8 / KVQ_BLOCK
+
+
+def kvq_append(cache: KVQCache, k, v, q=None, *, wq=None, wk=None, pos=None, n_new=None, start=None, eps=1e-6,
+               theta=500000.0, q_out=None, stream=None):
+    """ua_kvq_append: append k, v [B,T,Hkv,d] (the first n_new[b] tokens of sequence b), the keys
+    normalised (wk) and rotated on the way; start [B] int32 takes tokens back first.  With q [B,T,H,d]
+    the queries are normalised (wq) and rotated in the same launch and returned."""
+    if k is None or v is None:
+        raise ValueError("k and v are needed")
+    shape, dev = _qk_shape(q, k, wq, wk, pos, eps, theta, v)
+    if (shape.B, shape.Hkv, shape.d, k.dtype) != (cache.B, cache.Hkv, cache.d, cache.dtype):
+        raise ValueError(f"k: shape {tuple(k.shape)}, {k.dtype}, expected [{cache.B}, T, {cache.Hkv}, {cache.d}], {cache.dtype}")
+    if dev != cache.k.device:
+        raise ValueError(f"k: on {dev}, the cache is on {cache.k.device}")
+    _dense("n_new", n_new, (shape.B,), (torch.int32,), dev)
+    _dense("start", start, (shape.B,), (torch.int32,), dev)
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out: given without its input")
+    elif q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        _dense("q_out", q_out, q.shape, (q.dtype,), dev)
+    with torch.cuda.device(dev):
+        _check("ua_kvq_append", load_library().ua_kvq_append(
+            ctypes.byref(cache._struct), ctypes.byref(shape), _addr(q), k.data_ptr(), v.data_ptr(), _addr(wq), _addr(wk),
+            _addr(pos), _addr(n_new), _addr(start), _addr(q_out), _raw_stream(stream, dev)))
+    return q_out
+
+
+def kvq_attend_workspace_size(cache: KVQCache, H: int, Tq: int = 1) -> int:
+    """ua_kvq_attend_workspace_size: bytes of the attention's workspace (zeroed once, see alloc_workspace)."""
+    n = ctypes.c_size_t(0)
+    _check("ua_kvq_attend_workspace_size", load_library().ua_kvq_attend_workspace_size(
+        ctypes.byref(cache._struct), int(H), int(Tq), ctypes.byref(n)))
+    return n.value
+
+
+def kvq_attend(cache: KVQCache, q, *, g=None, bias=None, n_q=None, scale=None, out=None, lse=None, ws=None,
+               stream=None):
+    """ua_kvq_attend: attention of the last queries q [B,H,d] or [B,Tq,H,d] (the first n_q[b] of
+    them) over the cache.  bias [B,Hkv,capacity] f32 is added to the logits, g (like q) gates the output, lse
+    [B,H,Tq] f32 receives the row normalisers.  ws: kvq_attend_workspace_size bytes, zeroed once (a fresh
+    one is made without it).  Returns o, shaped like q."""
+    if q.dim() not in (3, 4):
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [B, H, d] or [B, Tq, H, d]")
+    dev = cache.k.device
+    B, Tq, H, d = q.shape if q.dim() == 4 else (q.shape[0], 1, q.shape[1], q.shape[2])
+    if (B, d) != (cache.B, cache.d):
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [{cache.B}, Tq, H, {cache.d}]")
+    act = (cache.dtype,)
+    _dense("q", q, q.shape, act, dev)
+    _dense("g", g, q.shape, act, dev)
+    _dense("bias", bias, (B, cache.Hkv, cache.capacity), F32, dev)
+    _dense("n_q", n_q, (B,), (torch.int32,), dev)
+    _dense("out", out, q.shape, act, dev)
+    _dense("lse", lse, (B, H, Tq), F32, dev)
+    o = out if out is not None else torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if ws is None:
+        ws = alloc_workspace(kvq_attend_workspace_size(cache, H, Tq), dev)
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous tensor on the call's device is needed")
+    with torch.cuda.device(dev):
+        _check("ua_kvq_attend", load_library().ua_kvq_attend(
+            ctypes.byref(cache._struct), H, Tq, q.data_ptr(), _addr(g), _addr(bias), _addr(n_q),
+            float(d) ** -0.5 if scale is None else float(scale), o.data_ptr(), _addr(lse), ws.data_ptr(), _nbytes(ws),
+            _raw_stream(stream, dev)))
     return o
 
 
