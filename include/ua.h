@@ -402,8 +402,8 @@ ua_status ua_qk_norm_rope_bwd(const ua_qk_shape* shape, const void* q, const voi
 /* ------------------------------------------------------------------ 8-bit cache
  * Slot j of sequence b holds the rotated key and the value of its j-th token.  Slots come in
  * blocks of 64 with one scale for each block and KV head, of keys and of values each:
- *   UA_KVQ_INT8: s = amax/127, code = round(x/s);  UA_KVQ_E4M3: s = the smallest power of two
- *   with amax/s <= 448, code = e4m3(x/s)           (round to nearest even; value = code * s;
+ *   UA_KVQ_INT8: s = amax/127, code = round(x * (127/amax));  UA_KVQ_E4M3: s = the smallest power
+ *   of two with amax/s <= 448, code = e4m3(x/s)    (fp32, round to nearest even; value = code * s;
  *   a block whose amax is below 2^-100 has s = 0)
  * A block is encoded once, when its 64th slot is filled, from rows kept until then in the
  * activation type: the unfinished block and the one before it live in a ring of 128 rows per

@@ -43,75 +43,95 @@ __device__ __forceinline__ SeqState seq_state(const KvqAppendParams& p, int b) {
     return s;
 }
 
-// Scale of a block from the bits of its largest magnitude, and the factor or divisor of the
-// encoding.  int8: s = amax / 127, x / s rounded.  e4m3: the format floats, so a power of two
-// loses nothing against amax / 448 and makes x / s exact: s = 2^(E - 8), or 2^(E - 7) where amax > 448 * 2^(E - 8)
-// (448 = 1.75 * 2^8), E the exponent of amax.
-template <bool E4M3> __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
-    if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);      // a value is not finite
-    if (amax_bits < 0x0d800000u) return 0.f;                                // below 2^-100
+// Scale of a block from the bits of its largest magnitude, and the factor of its encoding.  int8:
+// amax / 127 and 127 / amax.  e4m3: the format floats, so a power of two loses nothing against
+// amax / 448 and makes the scaling exact: 2^(E - 8), or 2^(E - 7) where amax > 448 * 2^(E - 8) (448 = 1.75 * 2^8), E
+// the exponent of amax; the factor is its reciprocal.  Factor 0 (all codes 0): a block of zeros (below 2^-100: scale 0) or with
+// a value that is not finite (scale NaN).
+template <bool E4M3> __device__ __forceinline__ float block_scale(uint32_t amax_bits, float* factor) {
+    *factor = 0.f;
+    if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
+    if (amax_bits < 0x0d800000u) return 0.f;
     if constexpr (E4M3) {
-        const int e = (int)(amax_bits >> 23) - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-        return __uint_as_float((uint32_t)e << 23);
+        const uint32_t e = (amax_bits >> 23) - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+        *factor = __uint_as_float((254 - e) << 23);
+        return __uint_as_float(e << 23);
     } else {
-        return __uint_as_float(amax_bits) / 127.f;
+        const float amax = __uint_as_float(amax_bits);
+        *factor = 127.f / amax;
+        return amax / 127.f;
     }
 }
 
 // 8 codes of a row's chunk
-template <bool E4M3> __device__ __forceinline__ uint2 encode8(const float* x, float s) {
+template <typename T, bool E4M3> __device__ __forceinline__ uint2 encode8(const Raw8<T>& raw, float factor) {
+    if (factor == 0.f) return make_uint2(0, 0);
+    float x[8];
+    raw.get(x);
     uint32_t w[2] = {0, 0};
-    if (s > 0.f) {                                       // (not for 0 or NaN: codes 0)
-        if constexpr (E4M3) {
-            const float inv = 1.f / s;                   // a power of two: exact
+    if constexpr (E4M3) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv),
-                                                             __NV_SATFINITE, __NV_E4M3);
-                w[i / 2] |= c2 << (16 * (i & 1));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int c = max(-127, min(127, __float2int_rn(x[i] / s)));
-                w[i / 4] |= (uint32_t)(c & 0xff) << (8 * (i & 3));
-            }
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * factor, x[2 * i + 1] * factor),
+                                                         __NV_SATFINITE, __NV_E4M3);
+            w[i / 2] |= c2 << (16 * (i & 1));
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)               // |x * factor| <= 127 (1 + 2^-23): rounds to 127 at most
+            w[i / 4] |= (uint32_t)(__float2int_rn(x[i] * factor) & 0xff) << (8 * (i & 3));
     }
     return make_uint2(w[0], w[1]);
 }
 
 // grid: B * (Hkv / hpc) * nb block CTAs, then q_tiles * q_split query CTAs; 4 * DH threads
+template <typename T> struct KvQueue {
+    static constexpr int NV = Raw8<T>::NV, DEPTH = 2;
+    template <int NTH> using Queue = LaneQueue<NTH, 4 * NV, DEPTH>;
+};
+
 template <typename T, int DH, bool E4M3>
-__global__ void __launch_bounds__(4 * DH) k_kvq_append(KvqAppendParams p) {
-    constexpr int CH = DH / 16, HALF = DH / 2, NW = 4 * DH / 32;
-    __shared__ float s_cos[kNormTokens * HALF], s_sin[kNormTokens * HALF];
+__global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppendParams p) {
+    constexpr int CH = DH / 16, HALF = DH / 2, NTH = 4 * DH, NW = NTH / 32, TOK = norm_tokens<DH, NTH>();
+    constexpr int NV = KvQueue<T>::NV, DEPTH = KvQueue<T>::DEPTH;
+    extern __shared__ __align__(16) unsigned char s_queue[];
+    __shared__ float s_cos[TOK * HALF], s_sin[TOK * HALF];
     __shared__ double s_f[HALF];
     __shared__ uint32_t s_max[2][2][NW];
     __shared__ int s_last;
     grid_dep_wait();
     const int tid = threadIdx.x, T_ = p.n.T, Hkv = p.c.Hkv;
     const int groups = Hkv / p.hpc, kv_ctas = p.c.B * groups * p.nb;
-    if ((int)blockIdx.x >= kv_ctas) {                    // queries
-        const int i = blockIdx.x - kv_ctas;
-        const long long n0 = (long long)(i / p.q_split) * kNormTokens;
-        float cs[8], sn[8];
-        if (p.n.rope) {
-            auto posf = [&](long long n) {
-                if (p.n.pos) return p.n.pos[n];
-                const int b = (int)(n / T_);
-                return (p.start ? p.start[b] : p.c.n_kept[b]) + (int)(n - (long long)b * T_);
-            };
-            tile_angles<DH>(s_cos, s_sin, n0, p.n.N, p.n.rf, s_f, posf, cs, sn);
+    // Every CTA arrives once it has read the slot counts; the last to arrive sets them, at its end.
+    auto arrive = [&]() {
+        if (tid == 0) {
+            __threadfence();
+            const int at = atomicAdd(p.c.ring_state + p.c.B, 1);
+            if (at >= (int)gridDim.x) raise_status(UA_ERR_INVALID_ARG);     // the counter did not start at 0
+            s_last = at == (int)gridDim.x - 1;
         }
+    };
+    if ((int)blockIdx.x >= kv_ctas) {                    // queries
+        const int i = blockIdx.x - kv_ctas, n0 = i / p.q_split * TOK;
         QkNormParams q = p.n;
         q.k = nullptr;
-        norm_rope_tile<T, DH>(q, n0, i % p.q_split, p.q_split, cs, sn);
+        NormTile<T, DH, NTH>::run(q, n0, i % p.q_split, p.q_split, s_queue, [&](float* cs, float* sn) {
+            auto posf = [&](int n) {
+                if (p.n.pos) return p.n.pos[n];
+                const int b = n / T_;
+                return (p.start ? p.start[b] : p.c.n_kept[b]) + n - b * T_;
+            };
+            if (p.n.rope) tile_angles<DH, NTH>(s_cos, s_sin, n0, (int)p.n.N, p.n.rf, s_f, posf, cs, sn);
+            arrive();                                    // (behind the angles' barrier)
+        });
     } else {
         const int j = blockIdx.x % p.nb, gi = (blockIdx.x / p.nb) % groups, b = blockIdx.x / p.nb / groups;
         const int row = tid / CH, c = tid % CH;
         const SeqState s = seq_state(p, b);
         if (s.refused && j == 0 && gi == 0 && tid == 0) raise_status(s.refused);
+        if (tid < HALF) s_f[tid] = p.n.rf.f[tid];
+        __syncthreads();
+        arrive();
         const int end = s.start + s.n_new, j0 = s.start / kKvqBlock, jl = end / kKvqBlock;   // jl: unfinished block
         const int mine = j0 + j;
         if (s.n_new > 0 && mine * kKvqBlock < end) {
@@ -120,20 +140,47 @@ __global__ void __launch_bounds__(4 * DH) k_kvq_append(KvqAppendParams p) {
             // that block's rows are then written by the first block's CTA, after it has read them.
             const bool old_rows = s.start % kKvqBlock != 0 && (j0 + 1) * kKvqBlock <= end;
             auto shares_first = [&](int blk) { return old_rows && blk > j0 && ((blk - j0) & 1) == 0; };
-            const int kept_here[2] = {mine >= jl - 1 && !shares_first(mine) ? mine : -1,
-                                      j == 0 ? (shares_first(jl) ? jl : shares_first(jl - 1) ? jl - 1 : -1) : -1};
-            if (tid < HALF) s_f[tid] = p.n.rf.f[tid];
-            __syncthreads();
+            const bool kept_here = mine >= jl - 1 && !shares_first(mine);
+            const int kept_too = j == 0 ? (shares_first(jl) ? jl : shares_first(jl - 1) ? jl - 1 : -1) : -1;
+            typename KvQueue<T>::template Queue<NTH> queue(s_queue);
             int buf = 0;
 #pragma unroll 1
             for (int pass = 0; pass < 2; ++pass) {
-                const int blk = pass == 0 ? mine : kept_here[1];
+                const int blk = pass == 0 ? mine : kept_too;
                 if (blk < 0) continue;
-                const bool keep = pass == 1 || kept_here[0] >= 0;
+                const bool keep = pass == 1 || kept_here;
                 const bool full = pass == 0 && (blk + 1) * kKvqBlock <= end;
                 const int slot = blk * kKvqBlock + row, t = slot - s.start;
                 const bool is_new = t >= 0 && slot < end, old = full && t < 0;
-                const long long n = (long long)b * T_ + t;
+                const int n = b * T_ + t;
+                // this thread's chunk in the ring, of head h: ring + h * kKvqRing * DH
+                const size_t ring = (((size_t)b * Hkv + gi * p.hpc) * kKvqRing + (slot & (kKvqRing - 1))) * DH + 8 * c;
+                T* kr = static_cast<T*>(p.c.kr) + ring;
+                T* vr = static_cast<T*>(p.c.vr) + ring;
+                const T* ksrc = old ? kr : static_cast<const T*>(p.n.k);
+                const T* vsrc = old ? vr : static_cast<const T*>(p.v);
+                if (is_new) {
+                    ksrc += (long long)n * p.n.k_ld + gi * p.hpc * DH + 8 * c;
+                    vsrc += (long long)n * p.v_ld + gi * p.hpc * DH + 8 * c;
+                }
+                const int hstep = old ? kKvqRing * DH : DH;
+                auto fetch = [&](int hh, int stage) {
+                    if (hh < p.hpc) {
+                        const bool ok = is_new || old;
+                        const T* k = ok ? ksrc + hh * hstep : ksrc;
+                        const T* v = ok ? vsrc + hh * hstep : vsrc;
+#pragma unroll
+                        for (int i = 0; i < NV; ++i) {
+                            queue.put(stage, i, k + i * Vec16<T>::N, ok);
+                            queue.put(stage, NV + i, k + HALF + i * Vec16<T>::N, ok);
+                            queue.put(stage, 2 * NV + i, v + i * Vec16<T>::N, ok);
+                            queue.put(stage, 3 * NV + i, v + HALF + i * Vec16<T>::N, ok);
+                        }
+                    }
+                    queue.commit();
+                };
+#pragma unroll
+                for (int i = 0; i < DEPTH - 1; ++i) fetch(i, i);
                 const long long crow = full ? kvq_row(p.c, b, blk) : -1;
                 float cs[8], sn[8];
                 if (p.n.rope && is_new) {
@@ -141,63 +188,50 @@ __global__ void __launch_bounds__(4 * DH) k_kvq_append(KvqAppendParams p) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) rope_cs_pi(pos, s_f[8 * c + e], cs + e, sn + e);
                 }
+                int stage = 0;
 #pragma unroll 1
                 for (int hh = 0; hh < p.hpc; ++hh) {
-                    const int h = gi * p.hpc + hh;
-                    const size_t ring = (((size_t)b * Hkv + h) * kKvqRing + (slot & (kKvqRing - 1))) * DH + 8 * c;
-                    T* kr = static_cast<T*>(p.c.kr) + ring;
-                    T* vr = static_cast<T*>(p.c.vr) + ring;
+                    fetch(hh + DEPTH - 1, (stage + DEPTH - 1) % DEPTH);
+                    queue.template wait<DEPTH - 1>();
                     Raw8<T> ka, kb, va, vb;
-                    ka.zero(); kb.zero(); va.zero(); vb.zero();
-                    if (is_new) {
-                        const T* ks = static_cast<const T*>(p.n.k) + n * p.n.k_ld + (long long)h * DH + 8 * c;
-                        const T* vs = static_cast<const T*>(p.v) + n * p.v_ld + (long long)h * DH + 8 * c;
-                        ka.ld(ks); kb.ld(ks + HALF);
-                        va.ld(vs); vb.ld(vs + HALF);
-                    } else if (old) {
-                        ka.ld(kr); kb.ld(kr + HALF);
-                        va.ld(vr); vb.ld(vr + HALF);
-                    }
-                    float x0[8], x1[8];
-                    ka.get(x0);
-                    kb.get(x1);
-                    {
-                        float y0[8], y1[8], w0[8], w1[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) { y0[e] = x0[e]; y1[e] = x1[e]; }
+                    for (int i = 0; i < NV; ++i) {
+                        ka.u[i] = queue.get(stage, i);
+                        kb.u[i] = queue.get(stage, NV + i);
+                    }
+                    if (p.n.wk != nullptr || p.n.rope) {
+                        float x0[8], x1[8];
+                        ka.get(x0);
+                        kb.get(x1);
                         if (p.n.wk != nullptr) {
+                            float w0[8], w1[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 w0[e] = __ldg(p.n.wk + 8 * c + e);
                                 w1[e] = __ldg(p.n.wk + HALF + 8 * c + e);
                             }
-                            norm_row<DH>(y0, y1, w0, w1, p.n.eps);
+                            norm_row<DH>(x0, x1, w0, w1, p.n.eps);
                         }
-                        if (is_new) {
-                            if (p.n.rope) rotate_row(y0, y1, cs, sn);
-                            ka.put(y0);                  // the cache holds the activation type: codes are
-                            kb.put(y1);                  // formed from the rounded key, however it came
-                            ka.get(x0);
-                            kb.get(x1);
+                        if (is_new) {                    // rounded to the activation type: codes are formed
+                            if (p.n.rope) rotate_row(x0, x1, cs, sn);       // from what the ring would hold
+                            ka.put(x0);
+                            kb.put(x1);
                         }
                     }
-                    if (full) {
-                        float z0[8], z1[8];
-                        va.get(z0);
-                        vb.get(z1);
-                        uint32_t mk = 0, mv = 0;         // non-negative floats order as their bits, NaN last
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            mk = max(mk, max(__float_as_uint(x0[e]) & 0x7fffffffu, __float_as_uint(x1[e]) & 0x7fffffffu));
-                            mv = max(mv, max(__float_as_uint(z0[e]) & 0x7fffffffu, __float_as_uint(z1[e]) & 0x7fffffffu));
-                        }
-                        mk = __reduce_max_sync(0xffffffffu, mk);
-                        mv = __reduce_max_sync(0xffffffffu, mv);
+                    for (int i = 0; i < NV; ++i) {
+                        va.u[i] = queue.get(stage, 2 * NV + i);
+                        vb.u[i] = queue.get(stage, 3 * NV + i);
+                    }
+                    stage = (stage + 1) % DEPTH;
+                    if (full) {
+                        uint32_t mk = __reduce_max_sync(0xffffffffu, max(ka.amax_bits(), kb.amax_bits()));
+                        uint32_t mv = __reduce_max_sync(0xffffffffu, max(va.amax_bits(), vb.amax_bits()));
                         if ((tid & 31) == 0) {
                             s_max[buf][0][tid >> 5] = mk;
                             s_max[buf][1][tid >> 5] = mv;
                         }
-                        __syncthreads();                 // (also: every earlier row has been read from the ring)
+                        __syncthreads();                 // (also: this head's earlier rows have been read from the ring)
 #pragma unroll
                         for (int i = 0; i < NW; ++i) {
                             mk = max(mk, s_max[buf][0][i]);
@@ -205,14 +239,15 @@ __global__ void __launch_bounds__(4 * DH) k_kvq_append(KvqAppendParams p) {
                         }
                         buf ^= 1;
                         if (crow >= 0) {
-                            const long long r = crow + (long long)h * p.c.bpp;
-                            const float sk = block_scale<E4M3>(mk), sv = block_scale<E4M3>(mv);
+                            const long long r = crow + (long long)(gi * p.hpc + hh) * p.c.bpp;
+                            float fk, fv;
+                            const float sk = block_scale<E4M3>(mk, &fk), sv = block_scale<E4M3>(mv, &fv);
                             uint8_t* dk = p.c.k + r * (kKvqBlock * DH) + row * DH + 8 * c;
                             uint8_t* dv = p.c.v + r * (kKvqBlock * DH) + row * DH + 8 * c;
-                            *reinterpret_cast<uint2*>(dk) = encode8<E4M3>(x0, sk);
-                            *reinterpret_cast<uint2*>(dk + HALF) = encode8<E4M3>(x1, sk);
-                            *reinterpret_cast<uint2*>(dv) = encode8<E4M3>(z0, sv);
-                            *reinterpret_cast<uint2*>(dv + HALF) = encode8<E4M3>(z1, sv);
+                            *reinterpret_cast<uint2*>(dk) = encode8<T, E4M3>(ka, fk);
+                            *reinterpret_cast<uint2*>(dk + HALF) = encode8<T, E4M3>(kb, fk);
+                            *reinterpret_cast<uint2*>(dv) = encode8<T, E4M3>(va, fv);
+                            *reinterpret_cast<uint2*>(dv + HALF) = encode8<T, E4M3>(vb, fv);
                             if (tid == 0) {
                                 p.c.ks[r] = sk;
                                 p.c.vs[r] = sv;
@@ -220,20 +255,16 @@ __global__ void __launch_bounds__(4 * DH) k_kvq_append(KvqAppendParams p) {
                         }
                     }
                     if (is_new && keep) {
-                        ka.st(kr); kb.st(kr + HALF);
-                        va.st(vr); vb.st(vr + HALF);
+                        T* kd = kr + (size_t)hh * kKvqRing * DH;
+                        T* vd = vr + (size_t)hh * kKvqRing * DH;
+                        ka.st(kd); kb.st(kd + HALF);
+                        va.st(vd); vb.st(vd + HALF);
                     }
                 }
+                queue.template wait<0>();
+                __syncthreads();                         // every earlier row of every head has been read
             }
         }
-    }
-    // The last CTA to arrive sets the slot counts: all others have read them.
-    __syncthreads();
-    if (tid == 0) {
-        __threadfence();
-        const int at = atomicAdd(p.c.ring_state + p.c.B, 1);
-        if (at >= (int)gridDim.x) raise_status(UA_ERR_INVALID_ARG);         // the counter did not start at 0
-        s_last = at == (int)gridDim.x - 1;
     }
     __syncthreads();
     if (s_last) {
@@ -250,8 +281,12 @@ __global__ void __launch_bounds__(4 * DH) k_kvq_append(KvqAppendParams p) {
 
 template <typename T, int DH, bool E4M3> cudaError_t append(const KvqAppendParams& p, cudaStream_t s) {
     const int ctas = p.c.B * (p.c.Hkv / p.hpc) * p.nb + p.q_tiles * p.q_split;
+    constexpr int q_smem = NormTile<T, DH, 4 * DH>::Queue::kBytes, kv_smem = KvQueue<T>::template Queue<4 * DH>::kBytes;
+    constexpr int smem = q_smem > kv_smem ? q_smem : kv_smem;
+    cudaError_t e = cudaFuncSetAttribute(k_kvq_append<T, DH, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
     UA_PROFILE("k_kvq_append", s);
-    return launch_dependent(k_kvq_append<T, DH, E4M3>, dim3(ctas), dim3(4 * DH), 0, s, p);
+    return launch_dependent(k_kvq_append<T, DH, E4M3>, dim3(ctas), dim3(4 * DH), smem, s, p);
 }
 
 template <typename T> cudaError_t append_t(const KvqAppendParams& p, int d, bool e4m3, cudaStream_t s) {

@@ -40,6 +40,21 @@ template <typename T> struct Raw8 {
                                   __float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3]));
         }
     }
+    // bits of the largest magnitude (non-negative floats order as their bits, NaN last)
+    __device__ __forceinline__ uint32_t amax_bits() const {
+        if constexpr (NV == 1) {
+            const uint32_t m = 0x7fff7fffu;
+            const uint32_t a = __vmaxu2(__vmaxu2(u[0].x & m, u[0].y & m), __vmaxu2(u[0].z & m, u[0].w & m));
+            return max(a & 0xffff0000u, a << 16);
+        } else {
+            uint32_t a = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                a = max(max(a, max(u[i].x & 0x7fffffffu, u[i].y & 0x7fffffffu)),
+                        max(u[i].z & 0x7fffffffu, u[i].w & 0x7fffffffu));
+            return a;
+        }
+    }
     __device__ __forceinline__ void st(T* p) const {
 #pragma unroll
         for (int i = 0; i < NV; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
@@ -83,24 +98,43 @@ __device__ __forceinline__ void rotate_row(float* x0, float* x1, const float* cs
     }
 }
 
-// Geometry of the norm kernels: 64 rows at a time in 64 * CH threads, as 16 tokens x 4 heads;
-// a thread keeps its token and chunk, so its 8 cosines and sines stay in registers while it
-// walks the heads four by four.
-constexpr int kNormTokens = 16, kNormHeads = 4;
+// Geometry of the norm kernels: NTH threads take NTH / CH rows at a time, as 4 heads of
+// NTH / CH / 4 tokens; a thread keeps its token and chunk, so its 8 cosines and sines stay in
+// registers while it walks the heads four by four.
+constexpr int kNormHeads = 4;
+template <int DH, int NTH> constexpr int norm_tokens() { return NTH / (DH / 16) / kNormHeads; }
 
-// cos / sin of a tile's tokens into shared memory ([16][DH/2] each), then this thread's eight.
+// A thread's own queue of 16-byte pieces in shared memory, filled by asynchronous copies several
+// steps ahead: loads in flight that cost no registers.  No other thread reads them, so a thread waits
+// for its own copies only.  Layout [stage][piece][thread]: neighbouring threads, neighbouring chunks.
+template <int NTH, int PIECES, int DEPTH> struct LaneQueue {
+    static constexpr int kBytes = NTH * PIECES * DEPTH * 16;
+    uint4* base;                                     // this thread's first piece
+    __device__ __forceinline__ LaneQueue(void* smem) : base(static_cast<uint4*>(smem) + threadIdx.x) {}
+    __device__ __forceinline__ void put(int stage, int piece, const void* src, bool ok) {
+        const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(base + (stage * PIECES + piece) * NTH));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+    }
+    __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    template <int PENDING> __device__ __forceinline__ void wait() {
+        asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+    }
+    __device__ __forceinline__ uint4 get(int stage, int piece) const { return base[(stage * PIECES + piece) * NTH]; }
+};
+
+// cos / sin of a tile's tokens into shared memory ([tokens][DH/2] each), then this thread's eight.
 // posf(n): position of flat token n.
-template <int DH, typename F>
-__device__ __forceinline__ void tile_angles(float* s_cos, float* s_sin, long long n0, long long N, const RopeFreq& rf,
+template <int DH, int NTH, typename F>
+__device__ __forceinline__ void tile_angles(float* s_cos, float* s_sin, int n0, int N, const RopeFreq& rf,
                                             double* s_f, F posf, float* cs, float* sn) {
-    constexpr int HALF = DH / 2, NTH = 64 * (DH / 16);
+    constexpr int HALF = DH / 2, TOK = norm_tokens<DH, NTH>();
     const int tid = threadIdx.x;
     if (tid < HALF) s_f[tid] = rf.f[tid];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kNormTokens * HALF / NTH; ++i) {
+    for (int i = 0; i < TOK * HALF / NTH; ++i) {
         const int e = i * NTH + tid, tk = e / HALF, m = e % HALF;
-        const long long n = n0 + tk;
+        const int n = n0 + tk;
         rope_cs_pi(n < N ? posf(n) : 0, s_f[m], s_cos + e, s_sin + e);
     }
     __syncthreads();
@@ -112,65 +146,77 @@ __device__ __forceinline__ void tile_angles(float* s_cos, float* s_sin, long lon
     }
 }
 
-// Forward of tokens n0 .. n0+15: head quads y, y + ny, ... of the queries, then of the keys.
-template <typename T, int DH>
-__device__ __forceinline__ void norm_rope_tile(const QkNormParams& p, long long n0, int y, int ny, const float* cs,
-                                               const float* sn) {
-    constexpr int CH = DH / 16, HALF = DH / 2;
-    const int tid = threadIdx.x, c = tid % CH, hp = (tid / CH) % kNormHeads;
-    const long long n = n0 + tid / CH / kNormHeads;
-    const int nq4 = p.q ? (p.H + kNormHeads - 1) / kNormHeads : 0;
-    const int nk4 = p.k ? (p.Hkv + kNormHeads - 1) / kNormHeads : 0;
-    auto src = [&](int i, bool* ok) -> const T* {
-        const bool is_q = i < nq4;
-        const int h = (is_q ? i : i - nq4) * kNormHeads + hp;
-        *ok = i < nq4 + nk4 && n < p.N && h < (is_q ? p.H : p.Hkv);
-        return is_q ? static_cast<const T*>(p.q) + n * p.q_ld + h * DH + 8 * c
-                    : static_cast<const T*>(p.k) + n * p.k_ld + h * DH + 8 * c;
-    };
-    Raw8<T> a, b;
-    bool ok;
-    const T* s = src(y, &ok);
-    a.zero();
-    b.zero();
-    if (ok) { a.ld(s); b.ld(s + HALF); }
-    float w0[8], w1[8];
-    const float* have = nullptr;                        // gain the registers hold
-    for (int i = y; i < nq4 + nk4; i += ny) {
-        Raw8<T> an, bn;                                 // the next quad's loads fly over this one's work
-        bool okn;
-        const T* sx = src(i + ny, &okn);
-        an.zero();
-        bn.zero();
-        if (okn) { an.ld(sx); bn.ld(sx + HALF); }
-        const bool is_q = i < nq4;
-        const float* w = is_q ? p.wq : p.wk;
-        if (w != nullptr && w != have) {
+// Forward of the tokens n0 ..: head quads y, y + ny, ... of the queries, then of the keys.
+// angles(cs, sn) is called once the first loads are on their way.
+template <typename T, int DH, int NTH> struct NormTile {
+    static constexpr int NV = Raw8<T>::NV, DEPTH = 4;
+    using Queue = LaneQueue<NTH, 2 * NV, DEPTH>;
+    template <typename A>
+    static __device__ __forceinline__ void run(const QkNormParams& p, int n0, int y, int ny, void* smem, A angles) {
+        constexpr int CH = DH / 16, HALF = DH / 2;
+        const int tid = threadIdx.x, c = tid % CH, hp = (tid / CH) % kNormHeads;
+        const int n = n0 + tid / CH / kNormHeads, N = (int)p.N;
+        const int nq4 = p.q ? (p.H + kNormHeads - 1) / kNormHeads : 0;
+        const int all = nq4 + (p.k ? (p.Hkv + kNormHeads - 1) / kNormHeads : 0);
+        Queue queue(smem);
+        auto fetch = [&](int i, int stage) {
+            if (i < all) {
+                const bool is_q = i < nq4;
+                const int h = (is_q ? i : i - nq4) * kNormHeads + hp;
+                const bool ok = n < N && h < (is_q ? p.H : p.Hkv);
+                const T* x = is_q ? static_cast<const T*>(p.q) : static_cast<const T*>(p.k);
+                const T* s = ok ? x + (long long)n * (is_q ? p.q_ld : p.k_ld) + h * DH + 8 * c : x;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                w0[e] = __ldg(w + 8 * c + e);
-                w1[e] = __ldg(w + HALF + 8 * c + e);
+                for (int v = 0; v < NV; ++v) {
+                    queue.put(stage, v, s + v * Vec16<T>::N, ok);
+                    queue.put(stage, NV + v, s + HALF + v * Vec16<T>::N, ok);
+                }
             }
-            have = w;
-        }
-        float x0[8], x1[8];
-        a.get(x0);
-        b.get(x1);
-        if (w != nullptr) norm_row<DH>(x0, x1, w0, w1, p.eps);
-        if (p.rope) rotate_row(x0, x1, cs, sn);
-        if (ok) {
+            queue.commit();
+        };
+#pragma unroll
+        for (int i = 0; i < DEPTH - 1; ++i) fetch(y + i * ny, i);
+        float cs[8], sn[8], w0[8], w1[8];
+        angles(cs, sn);
+        const float* have = nullptr;                    // gain the registers hold
+        int stage = 0;
+        for (int i = y; i < all; i += ny) {
+            const bool is_q = i < nq4;
+            const float* w = is_q ? p.wq : p.wk;
+            if (w != nullptr && w != have) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    w0[e] = __ldg(w + 8 * c + e);
+                    w1[e] = __ldg(w + HALF + 8 * c + e);
+                }
+                have = w;
+            }
+            fetch(i + (DEPTH - 1) * ny, (stage + DEPTH - 1) % DEPTH);
+            queue.template wait<DEPTH - 1>();
+            Raw8<T> a, b;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                a.u[v] = queue.get(stage, v);
+                b.u[v] = queue.get(stage, NV + v);
+            }
+            stage = (stage + 1) % DEPTH;
+            float x0[8], x1[8];
+            a.get(x0);
+            b.get(x1);
+            if (w != nullptr) norm_row<DH>(x0, x1, w0, w1, p.eps);
+            if (p.rope) rotate_row(x0, x1, cs, sn);
             const int h = (is_q ? i : i - nq4) * kNormHeads + hp;
-            T* d = is_q ? static_cast<T*>(p.q_out) + (n * p.H + h) * DH + 8 * c
-                        : static_cast<T*>(p.k_out) + (n * p.Hkv + h) * DH + 8 * c;
-            a.put(x0);
-            b.put(x1);
-            a.st(d);
-            b.st(d + HALF);
+            if (n < N && h < (is_q ? p.H : p.Hkv)) {
+                T* d = is_q ? static_cast<T*>(p.q_out) + ((long long)n * p.H + h) * DH + 8 * c
+                            : static_cast<T*>(p.k_out) + ((long long)n * p.Hkv + h) * DH + 8 * c;
+                a.put(x0);
+                b.put(x1);
+                a.st(d);
+                b.st(d + HALF);
+            }
         }
-        a = an;
-        b = bn;
-        ok = okn;
+        queue.template wait<0>();
     }
-}
+};
 
 }  // namespace ua

@@ -229,10 +229,7 @@ QkNormParams qk_params(const ua_qk_shape* s, const void* q, const void* k, const
     return p;
 }
 
-size_t qk_bwd_ws_bytes(const ua_qk_shape* s) {
-    const long long tiles = ((long long)s->B * s->T + 15) / 16;
-    return (size_t)std::min<long long>(tiles, kQkNormBwdCtas) * 2 * s->d * 4;
-}
+size_t qk_bwd_ws_bytes(const ua_qk_shape* s) { return (size_t)(kQkNormBwdCtas + 2) * s->d * 4; }
 
 ua_status check_kvq(const ua_kvq* c) {
     if (!c) return UA_ERR_INVALID_ARG;

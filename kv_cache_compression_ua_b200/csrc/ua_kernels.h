@@ -358,12 +358,12 @@ struct QkNormParams {
     void* dk;
     float* dwq;
     float* dwk;
-    float* part;                   // [CTAs][2][d] partial gain gradients
+    float* part;                   // [CTAs][d] partial gain gradients
     float eps;
     int rope;
     RopeFreq rf;
 };
-constexpr int kQkNormBwdCtas = 148 * 4;   // most CTAs of the backward (rows of `part`)
+constexpr int kQkNormBwdCtas = 148 * 2;   // CTAs of the backward (rows of `part`; one more where rounding gives it)
 cudaError_t launch_qk_norm_fwd(const QkNormParams& p, int d, bool bf16, cudaStream_t s);
 cudaError_t launch_qk_norm_bwd(const QkNormParams& p, int d, bool bf16, cudaStream_t s);
 

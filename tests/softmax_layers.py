@@ -76,7 +76,7 @@ def within(name, got, ref, bound, dtype):
 
 
 def encode(rows, fmt):
-    """A block [64, d] in the activation type -> (codes, scale), as the header defines them (fp32 division)."""
+    """A block [64, d] in the activation type -> (codes, scale), as the header defines them (in fp32)."""
     x = rows.detach().cpu().float()
     amax = x.abs().max()
     if not torch.isfinite(x).all():
@@ -85,7 +85,7 @@ def encode(rows, fmt):
         return torch.zeros(x.shape, dtype=torch.uint8), torch.tensor(0.0)
     if fmt == torch.int8:
         s = amax / 127.0
-        return torch.round(x / s).clamp(-127, 127).to(torch.int8).view(torch.uint8), s
+        return torch.round(x * torch.div(torch.tensor(127.0), amax)).to(torch.int8).view(torch.uint8), s
     e = -200
     while float(amax) / 2.0 ** e > 448.0:
         e += 1
