@@ -38,7 +38,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 14.f;             // probabilities are held as 2^14 p
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kRingBytes = 16384;           // per warp
-constexpr int kMinItems = kWarps;           // fewest blocks a CTA is given
+constexpr int kUnitCost = 6;                // what starting and merging a unit costs, in blocks
+constexpr int kMinItems = 10;               // fewest items (blocks and unit costs) a CTA is given
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -121,6 +122,10 @@ template <int DH> __device__ __forceinline__ int v_place(int tok, int chunk) {
 // rows 2c, 2c+1, 2c+8, 2c+9.
 __device__ __forceinline__ int tok_of(int r) { return (r >> 1) + ((r & 1) << 2); }
 
+// Place of an even element of O's row in shared memory: the rows 2c of a warp's store lie in
+// different banks.
+__device__ __forceinline__ int o_place(int row, int el) { return el ^ (row & 6); }
+
 template <typename T, int DH, int NT, bool E4M3> struct Att {
     static constexpr bool F32 = sizeof(T) == 4;
     static constexpr int R = 8 * NT;                 // query rows of a tile
@@ -134,15 +139,19 @@ template <typename T, int DH, int NT, bool E4M3> struct Att {
     static constexpr int NM = DH / 16;               // 16-element tiles of the output
     struct Smem {
         alignas(128) unsigned char ring[kWarps][kRingBytes];
+        alignas(16) float bias[kWarps][NSTG][kKvqBlock];
         alignas(16) uint16_t q16[QP][R][QS];         // f16, scaled by a power of two a row
         alignas(16) uint16_t qb[TP][R][QS];          // bf16 parts (for the unfinished block)
         float qf[R];                                 // logit scale times the row's power of two
         int lim[R];                                  // last slot the row sees, -1: none
         float m[kWarps][R], l[kWarps][R];
-        long long scan[kWarps];
+        alignas(16) float o[R][DH];                  // the CTA's sum of O, see o_place
+        int scan[kWarps];
         int found[2];
         int last;
     };
+    // CTAs an SM holds at once (228 KB of shared memory, 1 KB of each CTA's reserved)
+    static constexpr int CTAS = 3 * (sizeof(Smem) + 1024) <= 228 * 1024 ? 3 : 2;
 };
 
 // What a warp carries through a unit: O^T (elements 64 * pass + 8r + 2mt + {0, 1} of columns
@@ -152,10 +161,10 @@ template <int DH, int NT> struct State {
     float m[NT][2], l[NT][2];
 };
 
-// Online softmax of one block: logits x[mt][nt][e] (rows: tokens tok_of(r) and + 8, columns as in
-// State) -> probabilities in place, corr = factor of what was accumulated, any: whether the column sees the block.
-template <int DH, int NT>
-__device__ __forceinline__ void block_softmax(State<DH, NT>& st, float (&x)[4][NT][4], float (&corr)[NT][2],
+// Online softmax of 16 * MT tokens: logits x[mt][nt][e] (rows: tokens tok_of(r) and + 8, columns as
+// in State) -> 2^14 p in place, corr = factor of what was accumulated, any: whether the column sees one.
+template <int DH, int NT, int MT>
+__device__ __forceinline__ void block_softmax(State<DH, NT>& st, float (&x)[MT][NT][4], float (&corr)[NT][2],
                                               bool (&any)[NT][2]) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -163,24 +172,18 @@ __device__ __forceinline__ void block_softmax(State<DH, NT>& st, float (&x)[4][N
         for (int e = 0; e < 2; ++e) {
             float mx = x[0][nt][e];
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) mx = fmaxf(mx, fmaxf(x[mt][nt][e], x[mt][nt][e + 2]));
+            for (int mt = 0; mt < MT; ++mt) mx = fmaxf(mx, fmaxf(x[mt][nt][e], x[mt][nt][e + 2]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            // a NaN logit is no maximum, but it is something seen
-            bool seen = mx > -INFINITY;
-            bool nan = false;
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) nan |= x[mt][nt][e] != x[mt][nt][e] || x[mt][nt][e + 2] != x[mt][nt][e + 2];
-            const unsigned who = __ballot_sync(0xffffffffu, nan);
-            seen = seen || (who & (0x11111111u << (threadIdx.x & 3))) != 0;
-            any[nt][e] = seen;
+            // (a NaN logit is no maximum; it makes the sum NaN, and with it every output of the row)
+            any[nt][e] = mx > -INFINITY;
             const float mn = fmaxf(st.m[nt][e], mx);
             const float ms = mn == -INFINITY ? 0.f : mn;
             corr[nt][e] = ex2((st.m[nt][e] - ms) * kLog2e);
             st.m[nt][e] = mn;
             float sum = 0.f;
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     float& v = x[mt][nt][e + 2 * k];
@@ -206,374 +209,397 @@ template <int DH, int NT> __device__ __forceinline__ void init_state(State<DH, N
     }
 }
 
-// One unfinished block, its rows in the activation type out of the ring: bf16 products, the
-// operands as sums of bf16 parts (bf16 activations are one part, fp32 ones three; pairs of parts
-// below 2^-24 of the product are left out).  Read straight into the operands' registers: it is at
-// most one block in a unit.
+// A warp's 16 tokens of the unfinished block (slots slot0 .. of n), its rows in the activation type
+// in the warp's ring (kt, vt: [16][DH]; rows at and behind n are not there): bf16 products, the operands
+// as sums of bf16 parts (bf16 activations are one part, fp32 ones three; pairs of parts below 2^-24 of
+// the product are left out).
 template <typename T, int DH, int NT, bool E4M3>
-__device__ __forceinline__ void tail_block(const KvqAttendParams& p, typename Att<T, DH, NT, E4M3>::Smem& sm,
-                                        State<DH, NT>& st, int b, int h, int slot0, int n) {
+__device__ __forceinline__ void tail_part(const KvqAttendParams& p, typename Att<T, DH, NT, E4M3>::Smem& sm,
+                                          State<DH, NT>& st, const T* kt, const T* vt, const float* bias, int slot0,
+                                          int n) {
     using A = Att<T, DH, NT, E4M3>;
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const size_t ring = ((size_t)b * p.c.Hkv + h) * kKvqRing;
-    const T* kr = static_cast<const T*>(p.c.kr) + ring * DH;
-    const T* vr = static_cast<const T*>(p.c.vr) + ring * DH;
-    const int ring0 = slot0 & (kKvqRing - 1);
-    const float* bias = p.bias ? p.bias + ((size_t)b * p.c.Hkv + h) * p.c.cap + slot0 : nullptr;
-    float x[4][NT][4];
+    bool hidden[2];                                      // tokens no row sees: their rows may be anything
+    float bs[2];
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
+    for (int k = 0; k < 2; ++k) {
+        const int tok = tok_of(r) + 8 * k;
+        bs[k] = slot0 + tok >= n ? -INFINITY : bias ? bias[tok] : 0.f;
+        hidden[k] = bs[k] == -INFINITY;
+    }
+    float x[1][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[0][nt][e] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < DH / 16; ++s) {
+        const int d0 = (s >> 2) * 64 + 16 * c + 4 * (s & 3);
+        uint32_t a[A::TP][4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {                    // rows r and r + 8: elements d0 .. d0+3
+            const T* src = kt + (tok_of(r) + 8 * k) * DH + d0;
+            if constexpr (A::F32) {
+                const float4 f = *reinterpret_cast<const float4*>(src);
+                uint32_t lo[3], hi[3];
+                split_bf16<3>(f.x, f.y, lo);
+                split_bf16<3>(f.z, f.w, hi);
+#pragma unroll
+                for (int i = 0; i < A::TP; ++i) { a[i][k] = lo[i]; a[i][2 + k] = hi[i]; }
+            } else {
+                const uint2 u = *reinterpret_cast<const uint2*>(src);
+                a[0][k] = u.x;
+                a[0][2 + k] = u.y;
+            }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[mt][nt][e] = 0.f;
-        if (slot0 + 16 * mt < n) {
-#pragma unroll 4
-            for (int s = 0; s < DH / 16; ++s) {
-                const int d0 = (s >> 2) * 64 + 16 * c + 4 * (s & 3);
-                uint32_t a[A::TP][4];
+            for (int j = 0; j < A::TP; ++j) {
+                const uint2 q = *reinterpret_cast<const uint2*>(&sm.qb[j][8 * nt + r][d0]);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {            // rows r and r + 8: elements d0 .. d0+3
-                    const int tok = 16 * mt + tok_of(r) + 8 * k;
-                    const bool ok = slot0 + tok < n;
-                    const T* src = kr + (size_t)(ring0 + tok) * DH + d0;
-                    if constexpr (A::F32) {
-                        const float4 f = ok ? *reinterpret_cast<const float4*>(src) : make_float4(0, 0, 0, 0);
-                        uint32_t lo[3], hi[3];
-                        split_bf16<3>(f.x, f.y, lo);
-                        split_bf16<3>(f.z, f.w, hi);
-#pragma unroll
-                        for (int i = 0; i < A::TP; ++i) { a[i][k] = lo[i]; a[i][2 + k] = hi[i]; }
-                    } else {
-                        const uint2 u = ok ? *reinterpret_cast<const uint2*>(src) : make_uint2(0, 0);
-                        a[0][k] = u.x;
-                        a[0][2 + k] = u.y;
-                    }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < A::TP; ++j) {
-                        const uint2 q = *reinterpret_cast<const uint2*>(&sm.qb[j][8 * nt + r][d0]);
-#pragma unroll
-                        for (int i = 0; i + j < A::TP; ++i) mma_bf16(x[mt][nt], a[i], q);
-                    }
+                for (int i = 0; i + j < A::TP; ++i) mma_bf16(x[0][nt], a[i], q);
             }
-        }
     }
-    bool hidden[4][2];                                   // tokens no row sees: their values may be anything
+    // a token's row of the values' operand sits at other lanes than its logit: the bit of token t comes
+    // from lane 4 row, tok_of(row) = t mod 8
+    const unsigned hid[2] = {__ballot_sync(0xffffffffu, hidden[0]), __ballot_sync(0xffffffffu, hidden[1])};
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int tok = 16 * mt + tok_of(r) + 8 * k, slot = slot0 + tok;
-            const float bs = slot >= n ? -INFINITY : bias ? __ldg(bias + tok) : 0.f;
-            hidden[mt][k] = bs == -INFINITY;
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float& v = x[mt][nt][2 * k + e];
-                    v = hidden[mt][k] || slot > sm.lim[8 * nt + 2 * c + e] ? -INFINITY : fmaf(v, p.scale, bs);
-                }
-        }
+            for (int e = 0; e < 2; ++e) {
+                float& v = x[0][nt][2 * k + e];
+                v = hidden[k] || slot0 + tok_of(r) + 8 * k > sm.lim[8 * nt + 2 * c + e] ? -INFINITY
+                                                                                       : fmaf(v, p.scale, bs[k]);
+            }
     float corr[NT][2];
     bool any[NT][2];
-    block_softmax<DH, NT>(st, x, corr, any);
-    uint2 pb[A::TPP][4][NT];
+    block_softmax<DH, NT, 1>(st, x, corr, any);
+    uint2 pb[A::TPP][NT];
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
+    for (int nt = 0; nt < NT; ++nt) {
+        uint32_t lo[A::TPP], hi[A::TPP];
+        split_bf16<A::TPP>(x[0][nt][0], x[0][nt][1], lo);
+        split_bf16<A::TPP>(x[0][nt][2], x[0][nt][3], hi);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            uint32_t lo[A::TPP], hi[A::TPP];
-            split_bf16<A::TPP>(x[mt][nt][0], x[mt][nt][1], lo);
-            split_bf16<A::TPP>(x[mt][nt][2], x[mt][nt][3], hi);
-#pragma unroll
-            for (int i = 0; i < A::TPP; ++i) pb[i][mt][nt] = make_uint2(transpose8x8(lo[i]), transpose8x8(hi[i]));
-        }
-    // a token's row of the values' operand sits at other lanes than its logit: the bit of token
-    // 16 ks + t comes from lane 4 r(t) of the same 16 tokens
-    unsigned hid[4][2];
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) hid[ks][k] = __ballot_sync(0xffffffffu, hidden[ks][k]);
+        for (int i = 0; i < A::TPP; ++i) pb[i][nt] = make_uint2(transpose8x8(lo[i]), transpose8x8(hi[i]));
+    }
 #pragma unroll
     for (int pass = 0; pass < DH / 64; ++pass) {
-        float acc[4][NT][4];
+        float v[4][8];                                   // tokens 4i + c, elements 64 pass + 8r ..
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
+        for (int i = 0; i < 4; ++i) {
+            const int t = 4 * i + c, row = 2 * (t & 3) + ((t >> 2) & 1);
+            const T* src = vt + t * DH + 64 * pass + 8 * r;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            if (slot0 + 16 * ks >= n) continue;
-            float v[4][8];                               // tokens 4i + c, elements 64 pass + 8r ..
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 4 * i + c;                 // row of the logits' operand: tok_of(row) = t mod 8
-                const int row = 2 * (t & 3) + ((t >> 2) & 1);
-                const bool ok = ((hid[ks][t >> 3] >> (4 * row)) & 1u) == 0;
-                const T* src = vr + (size_t)(ring0 + 16 * ks + t) * DH + 64 * pass + 8 * r;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-                if (ok) {
-                    Vec16<T>::ld(src, v[i]);
-                    if constexpr (A::F32) Vec16<T>::ld(src + 4, v[i] + 4);
-                }
+            for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+            if (((hid[t >> 3] >> (4 * row)) & 1u) == 0) {
+                Vec16<T>::ld(src, v[i]);
+                if constexpr (A::F32) Vec16<T>::ld(src + 4, v[i] + 4);
             }
+        }
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                uint32_t a[4][A::TP];
+        for (int mt = 0; mt < 4; ++mt) {
+            uint32_t a[4][A::TP];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    split_bf16<A::TP>(v[0][2 * mt + k], v[1][2 * mt + k], a[k]);
-                    split_bf16<A::TP>(v[2][2 * mt + k], v[3][2 * mt + k], a[2 + k]);
-                }
+            for (int k = 0; k < 2; ++k) {
+                split_bf16<A::TP>(v[0][2 * mt + k], v[1][2 * mt + k], a[k]);
+                split_bf16<A::TP>(v[2][2 * mt + k], v[3][2 * mt + k], a[2 + k]);
+            }
+            float acc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
 #pragma unroll
                 for (int i = 0; i < A::TP; ++i) {
                     const uint32_t ai[4] = {a[0][i], a[1][i], a[2][i], a[3][i]};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int j = 0; j < A::TPP; ++j)
-                            if (i + j < 3) mma_bf16(acc[mt][nt], ai, pb[j][ks][nt]);
+                    for (int j = 0; j < A::TPP; ++j)
+                        if (i + j < 3) mma_bf16(acc[nt], ai, pb[j][nt]);
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    st.o[4 * pass + mt][nt][e] =
+                        fmaf(st.o[4 * pass + mt][nt][e], corr[nt][e & 1], any[nt][e & 1] ? acc[nt][e] : 0.f);
             }
         }
+    }
+}
+
+// The warp's walk through one unit: the finished blocks first, first + kWarps, ... < last, then its 16
+// tokens of the unfinished block if the CTA's run ends with it.  begin() starts the first copies; run()
+// needs the queries in shared memory.
+template <typename T, int DH, int NT, bool E4M3> struct Walk {
+    using A = Att<T, DH, NT, E4M3>;
+    static constexpr long long kNone = -1, kTail = -2, kNoPage = -3;
+    static_assert(16 * DH * sizeof(T) <= A::KB, "a warp's rows of the unfinished block fit a block's place");
+    const KvqAttendParams& p;
+    typename A::Smem& sm;
+    const int warp, lane, r, c;
+    int b, first, steps, full, slot0, n;             // steps: blocks and the 16 tokens; full: blocks
+    long long unit, hrow, rows[A::NSTG + 1];         // code rows of the steps in flight and of the one after
+    const float* bias0;
+    float ks, vs;
+
+    __device__ __forceinline__ Walk(const KvqAttendParams& p_, typename A::Smem& sm_)
+        : p(p_), sm(sm_), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), r(lane >> 2), c(lane & 3) {}
+
+    __device__ __forceinline__ long long row_of(int i) const {
+        if (i >= full) return i < steps ? kTail : kNone;
+        const long long x = kvq_row(p.c, b, first + i * kWarps);
+        return x < 0 ? kNoPage : x + hrow;
+    }
+    // step i's keys (and bias) / values into place stg
+    __device__ __forceinline__ void load_k(long long row, int i, int stg) {
+        const uint32_t dst = tc::smem_u32(sm.ring[warp]) + stg * 2 * A::KB;
+        if (row >= 0) {
+            const uint8_t* src = p.c.k + row * A::KB;
+#pragma unroll
+            for (int j = 0; j < A::KB / 512; ++j) {
+                const int e = j * 32 + lane, tok = e / (DH / 16), ch = e % (DH / 16);
+                cp_async16(dst + k_place<DH>(tok, ch), src + e * 16);
+            }
+            if (bias0 && lane < 16)
+                cp_async16(tc::smem_u32(&sm.bias[warp][stg][4 * lane]), bias0 + (first + i * kWarps) * kKvqBlock + 4 * lane);
+        } else if (row == kTail) {
+            load_tail(dst, p.c.kr);
+            if (bias0 && lane < 4) cp_async16(tc::smem_u32(&sm.bias[warp][stg][4 * lane]), bias0 + slot0 + 4 * lane);
+        }
+        tc::cp_async_commit();
+    }
+    __device__ __forceinline__ void load_v(long long row, int stg) {
+        const uint32_t dst = tc::smem_u32(sm.ring[warp]) + (stg * 2 + 1) * A::KB;
+        if (row >= 0) {
+            const uint8_t* src = p.c.v + row * A::KB;
+#pragma unroll
+            for (int j = 0; j < A::KB / 512; ++j) {
+                const int e = j * 32 + lane, tok = e / (DH / 16), ch = e % (DH / 16);
+                cp_async16(dst + v_place<DH>(tok, ch), src + e * 16);
+            }
+        } else if (row == kTail) {
+            load_tail(dst, p.c.vr);
+        }
+        tc::cp_async_commit();
+    }
+    __device__ __forceinline__ void load_tail(uint32_t dst, const void* ring) {
+        constexpr int PER = DH * (int)sizeof(T) / 16;    // 16-byte pieces of a row
+        const T* src = static_cast<const T*>(ring) + (unit * kKvqRing + (slot0 & (kKvqRing - 1))) * DH;
+        const int left = (n - slot0) * PER;
+#pragma unroll
+        for (int j = 0; j < 16 * PER / 32; ++j) {
+            const int e = j * 32 + lane;
+            if (e < left) cp_async16(dst + e * 16, reinterpret_cast<const uint4*>(src) + e);
+        }
+    }
+    // blocks first_ .. last_ - 1 and, with_tail, the unfinished block of n_ slots
+    __device__ __forceinline__ void begin(int b_, int h, int first_, int last_, bool with_tail, int n_) {
+        b = b_;
+        first = first_;
+        n = n_;
+        full = max(0, (last_ - first + kWarps - 1) / kWarps);
+        slot0 = n / kKvqBlock * kKvqBlock + 16 * warp;
+        steps = full + (with_tail && slot0 < n ? 1 : 0);
+        unit = (long long)b * p.c.Hkv + h;
+        hrow = (long long)h * p.c.bpp;
+        bias0 = p.bias ? p.bias + unit * p.c.cap : nullptr;
+#pragma unroll
+        for (int i = 0; i <= A::NSTG; ++i) rows[i] = row_of(i);
+#pragma unroll
+        for (int i = 0; i < A::NSTG; ++i) {
+            load_k(rows[i], i, i);
+            load_v(rows[i], i);
+        }
+        ks = rows[0] >= 0 ? __ldg(p.c.ks + rows[0]) : 0.f;
+        vs = rows[0] >= 0 ? __ldg(p.c.vs + rows[0]) : 0.f;
+    }
+    __device__ __forceinline__ void run(State<DH, NT>& st) {
+        float qf[NT][2];
+        int lim[NT][2], lim_min = INT32_MAX;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                qf[nt][e] = sm.qf[8 * nt + 2 * c + e];
+                lim[nt][e] = sm.lim[8 * nt + 2 * c + e];
+                lim_min = min(lim_min, lim[nt][e]);
+            }
+        lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+        int stg = 0;
+#pragma unroll 1
+        for (int i = 0; i < steps; ++i) {
+            const long long row = rows[0], next = rows[A::NSTG];
+#pragma unroll
+            for (int k = 0; k < A::NSTG; ++k) rows[k] = rows[k + 1];
+            rows[A::NSTG] = row_of(i + A::NSTG + 1);
+            const float ksn = rows[0] >= 0 ? __ldg(p.c.ks + rows[0]) : 0.f;
+            const float vsn = rows[0] >= 0 ? __ldg(p.c.vs + rows[0]) : 0.f;
+            if (row >= 0) {
+                block(st, i, next, stg, qf, lim, lim_min);
+            } else {
+                if (row == kTail) {                      // the last step
+                    cp_async_wait<0>();
+                    __syncwarp();
+                    const unsigned char* at = sm.ring[warp] + stg * 2 * A::KB;
+                    tail_part<T, DH, NT, E4M3>(p, sm, st, reinterpret_cast<const T*>(at),
+                                               reinterpret_cast<const T*>(at + A::KB),
+                                               bias0 ? sm.bias[warp][stg] : nullptr, slot0, n);
+                }
+                load_k(next, i + A::NSTG, stg);          // (no page: left out)
+                load_v(next, stg);
+            }
+            ks = ksn;
+            vs = vsn;
+            stg = stg + 1 == A::NSTG ? 0 : stg + 1;
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+    }
+    __device__ __forceinline__ void block(State<DH, NT>& st, int i, long long next, int stg, const float (&qf)[NT][2],
+                                          const int (&lim)[NT][2], int lim_min) {
+        const int blk = first + i * kWarps;
+        const unsigned char* kb = sm.ring[warp] + stg * 2 * A::KB;
+        const unsigned char* vb = kb + A::KB;
+        // S^T = K Q^T
+        cp_async_wait<2 * A::NSTG - 1>();
+        __syncwarp();
+        float x[4][NT][4];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    st.o[4 * pass + mt][nt][e] =
-                        fmaf(st.o[4 * pass + mt][nt][e], corr[nt][e & 1], any[nt][e & 1] ? acc[mt][nt][e] : 0.f);
-    }
-}
-
-// The warp's walk over blocks first, first + kWarps, ... < last of one unit.
-template <typename T, int DH, int NT, bool E4M3>
-__device__ __forceinline__ void walk(const KvqAttendParams& p, typename Att<T, DH, NT, E4M3>::Smem& sm,
-                                     State<DH, NT>& st, int b, int h, int n, int first, int last) {
-    using A = Att<T, DH, NT, E4M3>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const int nfull = n / kKvqBlock;
-    const long long hrow = (long long)h * p.c.bpp;
-    unsigned char* ring = sm.ring[warp];
-    const uint32_t ring_s = tc::smem_u32(ring);
-    const float* bias0 = p.bias ? p.bias + ((size_t)b * p.c.Hkv + h) * p.c.cap : nullptr;
-    // row of block i (or -1: past the run, the unfinished block, or a bad page)
-    auto row_of = [&](int blk) -> long long {
-        if (blk >= last || blk >= nfull) return -1;
-        const long long x = kvq_row(p.c, b, blk);
-        return x < 0 ? -1 : x + hrow;
-    };
-    auto load_k = [&](long long row, int stg) {
-        if (row >= 0) {
-            const uint8_t* src = p.c.k + row * A::KB;
+                for (int e = 0; e < 4; ++e) x[mt][nt][e] = 0.f;
 #pragma unroll
-            for (int i = 0; i < A::KB / 512; ++i) {
-                const int e = i * 32 + lane, tok = e / (DH / 16), ch = e % (DH / 16);
-                cp_async16(ring_s + stg * 2 * A::KB + k_place<DH>(tok, ch), src + e * 16);
+        for (int hf = 0; hf < DH / 64; ++hf) {
+            uint2 q[A::QP][NT][4];
+#pragma unroll
+            for (int i = 0; i < A::QP; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        q[i][nt][s] = *reinterpret_cast<const uint2*>(&sm.q16[i][8 * nt + r][64 * hf + 16 * c + 4 * s]);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+                const int tok = 16 * mt + tok_of(r);
+                const uint4 u0 = *reinterpret_cast<const uint4*>(kb + k_place<DH>(tok, 4 * hf + c));
+                const uint4 u1 = *reinterpret_cast<const uint4*>(kb + k_place<DH>(tok + 8, 4 * hf + c));
+                const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    uint32_t a[4];
+                    codes_f16<E4M3>(w0[s], a[0], a[2]);
+                    codes_f16<E4M3>(w1[s], a[1], a[3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < A::QP; ++i) mma_f16(x[mt][nt], a, q[i][nt][s]);
+                }
             }
         }
-        tc::cp_async_commit();
-    };
-    auto load_v = [&](long long row, int stg) {
-        if (row >= 0) {
-            const uint8_t* src = p.c.v + row * A::KB;
+        float bs[4][2];
+        if (bias0) {
 #pragma unroll
-            for (int i = 0; i < A::KB / 512; ++i) {
-                const int e = i * 32 + lane, tok = e / (DH / 16), ch = e % (DH / 16);
-                cp_async16(ring_s + (stg * 2 + 1) * A::KB + v_place<DH>(tok, ch), src + e * 16);
-            }
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) bs[mt][k] = sm.bias[warp][stg][16 * mt + tok_of(r) + 8 * k];
         }
-        tc::cp_async_commit();
-    };
-    // rows of the blocks in flight, and the scales of the next block, are fetched ahead
-    long long rows[A::NSTG + 1];
+        __syncwarp();
+        load_k(next, i + A::NSTG, stg);
+        // logits
+        const bool masked = blk * kKvqBlock + kKvqBlock - 1 > lim_min;
 #pragma unroll
-    for (int i = 0; i <= A::NSTG; ++i) rows[i] = row_of(first + i * kWarps);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < A::NSTG; ++i) {
-        load_k(rows[i], i);
-        load_v(rows[i], i);
-    }
-    float ks = rows[0] >= 0 ? __ldg(p.c.ks + rows[0]) : 0.f, vs = rows[0] >= 0 ? __ldg(p.c.vs + rows[0]) : 0.f;
-    float qf[NT][2];
-    int lim[NT][2], lim_min = INT32_MAX;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            qf[nt][e] = sm.qf[8 * nt + 2 * c + e];
-            lim[nt][e] = sm.lim[8 * nt + 2 * c + e];
-            lim_min = min(lim_min, lim[nt][e]);
-        }
-    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
-    int stg = 0;
-#pragma unroll 1
-    for (int blk = first; blk < last; blk += kWarps) {
-        const long long row = rows[0], next = rows[A::NSTG];
-#pragma unroll
-        for (int i = 0; i < A::NSTG; ++i) rows[i] = rows[i + 1];
-        rows[A::NSTG] = row_of(blk + (A::NSTG + 1) * kWarps);
-        const float ksn = rows[0] >= 0 ? __ldg(p.c.ks + rows[0]) : 0.f;
-        const float vsn = rows[0] >= 0 ? __ldg(p.c.vs + rows[0]) : 0.f;
-        if (row < 0) {                                   // the unfinished block, or one without a page
-            if (blk == nfull) tail_block<T, DH, NT, E4M3>(p, sm, st, b, h, blk * kKvqBlock, n);
-            load_k(next, stg);
-            load_v(next, stg);
-        } else {
-            const unsigned char* kb = ring + stg * 2 * A::KB;
-            const unsigned char* vb = kb + A::KB;
-            float bs[4][2];
-            if (bias0) {
+            for (int e = 0; e < 2; ++e) {
+                const float f = qf[nt][e] * ks;
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        bs[mt][k] = __ldg(bias0 + blk * kKvqBlock + 16 * mt + tok_of(r) + 8 * k);
+                    for (int k = 0; k < 2; ++k) {
+                        float& v = x[mt][nt][2 * k + e];
+                        v *= f;
+                        if (bias0) v = bs[mt][k] == -INFINITY ? -INFINITY : v + bs[mt][k];
+                        if (masked && blk * kKvqBlock + 16 * mt + tok_of(r) + 8 * k > lim[nt][e]) v = -INFINITY;
+                    }
             }
-            // S^T = K Q^T
-            cp_async_wait<2 * A::NSTG - 1>();
-            __syncwarp();
-            float x[4][NT][4];
+        float corr[NT][2];
+        bool any[NT][2];
+        block_softmax<DH, NT, 4>(st, x, corr, any);
+        uint2 pb[A::PP][4][NT];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t lo = pack_f16(x[mt][nt][0], x[mt][nt][1]), hi = pack_f16(x[mt][nt][2], x[mt][nt][3]);
+                pb[0][mt][nt] = make_uint2(transpose8x8(lo), transpose8x8(hi));
+                if constexpr (A::PP == 2) {
+                    const float2 l2 = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+                    const float2 h2 = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                    pb[1][mt][nt] = make_uint2(transpose8x8(pack_f16(x[mt][nt][0] - l2.x, x[mt][nt][1] - l2.y)),
+                                               transpose8x8(pack_f16(x[mt][nt][2] - h2.x, x[mt][nt][3] - h2.y)));
+                }
+            }
+        // O^T += vs * V^T P^T
+        cp_async_wait<2 * A::NSTG - 1>();
+        __syncwarp();
+#pragma unroll
+        for (int pass = 0; pass < DH / 64; ++pass) {
+            float acc[4][NT][4];
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[mt][nt][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
 #pragma unroll
-            for (int hf = 0; hf < DH / 64; ++hf) {
-                uint2 q[A::QP][NT][4];
+            for (int kt = 0; kt < 4; ++kt) {
+                uint2 w[4];                          // tokens 4i + c, elements 64 pass + 8r ..
 #pragma unroll
-                for (int i = 0; i < A::QP; ++i)
+                for (int i = 0; i < 4; ++i)
+                    w[i] = *reinterpret_cast<const uint2*>(vb + v_place<DH>(16 * kt + 4 * i + c, 4 * pass + (r >> 1)) +
+                                                           8 * (r & 1));
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                for (int hw = 0; hw < 2; ++hw) {
+                    const uint32_t t0 = hw ? w[0].y : w[0].x, t1 = hw ? w[1].y : w[1].x;
+                    const uint32_t t2 = hw ? w[2].y : w[2].x, t3 = hw ? w[3].y : w[3].x;
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            q[i][nt][s] = *reinterpret_cast<const uint2*>(&sm.q16[i][8 * nt + r][64 * hf + 16 * c + 4 * s]);
-#pragma unroll
-                for (int mt = 0; mt < 4; ++mt) {
-                    const int tok = 16 * mt + tok_of(r);
-                    const uint4 u0 = *reinterpret_cast<const uint4*>(kb + k_place<DH>(tok, 4 * hf + c));
-                    const uint4 u1 = *reinterpret_cast<const uint4*>(kb + k_place<DH>(tok + 8, 4 * hf + c));
-                    const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
+                    for (int k = 0; k < 2; ++k) {
                         uint32_t a[4];
-                        codes_f16<E4M3>(w0[s], a[0], a[2]);
-                        codes_f16<E4M3>(w1[s], a[1], a[3]);
+                        const uint32_t sel = k ? 0x7362 : 0x5140;
+                        codes_f16<E4M3>(__byte_perm(t0, t1, sel), a[0], a[1]);
+                        codes_f16<E4M3>(__byte_perm(t2, t3, sel), a[2], a[3]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int i = 0; i < A::QP; ++i) mma_f16(x[mt][nt], a, q[i][nt][s]);
+                            for (int i = 0; i < A::PP; ++i) mma_f16(acc[2 * hw + k][nt], a, pb[i][kt][nt]);
                     }
                 }
             }
-            __syncwarp();
-            load_k(next, stg);
-            // logits
-            const bool masked = blk * kKvqBlock + kKvqBlock - 1 > lim_min;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float f = qf[nt][e] * ks;
+                    const float f = any[nt][e] ? vs : 0.f;   // (a block no slot of which is seen may have a NaN scale)
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            float& v = x[mt][nt][2 * k + e];
-                            v *= f;
-                            if (bias0) v = bs[mt][k] == -INFINITY ? -INFINITY : v + bs[mt][k];
-                            if (masked && blk * kKvqBlock + 16 * mt + tok_of(r) + 8 * k > lim[nt][e]) v = -INFINITY;
+                            float& o = st.o[4 * pass + mt][nt][2 * k + e];
+                            o = fmaf(acc[mt][nt][2 * k + e], f, o * corr[nt][e]);
                         }
                 }
-            float corr[NT][2];
-            bool any[NT][2];
-            block_softmax<DH, NT>(st, x, corr, any);
-            uint2 pb[A::PP][4][NT];
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint32_t lo = pack_f16(x[mt][nt][0], x[mt][nt][1]), hi = pack_f16(x[mt][nt][2], x[mt][nt][3]);
-                    pb[0][mt][nt] = make_uint2(transpose8x8(lo), transpose8x8(hi));
-                    if constexpr (A::PP == 2) {
-                        const float2 l2 = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-                        const float2 h2 = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-                        pb[1][mt][nt] = make_uint2(transpose8x8(pack_f16(x[mt][nt][0] - l2.x, x[mt][nt][1] - l2.y)),
-                                                   transpose8x8(pack_f16(x[mt][nt][2] - h2.x, x[mt][nt][3] - h2.y)));
-                    }
-                }
-            // O^T += vs * V^T P^T
-            cp_async_wait<2 * A::NSTG - 1>();
-            __syncwarp();
-#pragma unroll
-            for (int pass = 0; pass < DH / 64; ++pass) {
-                float acc[4][NT][4];
-#pragma unroll
-                for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
-#pragma unroll
-                for (int kt = 0; kt < 4; ++kt) {
-                    uint2 w[4];                          // tokens 4i + c, elements 64 pass + 8r ..
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        w[i] = *reinterpret_cast<const uint2*>(vb + v_place<DH>(16 * kt + 4 * i + c, 4 * pass + (r >> 1)) +
-                                                               8 * (r & 1));
-#pragma unroll
-                    for (int hw = 0; hw < 2; ++hw) {
-                        const uint32_t t0 = hw ? w[0].y : w[0].x, t1 = hw ? w[1].y : w[1].x;
-                        const uint32_t t2 = hw ? w[2].y : w[2].x, t3 = hw ? w[3].y : w[3].x;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            uint32_t a[4];
-                            const uint32_t sel = k ? 0x7362 : 0x5140;
-                            codes_f16<E4M3>(__byte_perm(t0, t1, sel), a[0], a[1]);
-                            codes_f16<E4M3>(__byte_perm(t2, t3, sel), a[2], a[3]);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int i = 0; i < A::PP; ++i) mma_f16(acc[2 * hw + k][nt], a, pb[i][kt][nt]);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float f = any[nt][e] ? vs : 0.f;   // (a block no slot of which is seen may have a NaN scale)
-#pragma unroll
-                        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                float& o = st.o[4 * pass + mt][nt][2 * k + e];
-                                o = fmaf(acc[mt][nt][2 * k + e], f, o * corr[nt][e]);
-                            }
-                    }
-            }
-            __syncwarp();
-            load_v(next, stg);
         }
-        ks = ksn;
-        vs = vsn;
-        stg = stg + 1 == A::NSTG ? 0 : stg + 1;
+        __syncwarp();
+        load_v(next, stg);
     }
-    cp_async_wait<0>();
-}
+};
 
 template <typename T, int DH, int NT, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 3) k_kvq_attend(KvqAttendParams p) {
+__global__ void __launch_bounds__(kThreads, Att<T, DH, NT, E4M3>::CTAS) k_kvq_attend(KvqAttendParams p) {
     using A = Att<T, DH, NT, E4M3>;
     constexpr int R = A::R;
     extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -593,86 +619,117 @@ __global__ void __launch_bounds__(kThreads, 3) k_kvq_attend(KvqAttendParams p) {
     };
     auto tiles_of = [&](int nq) { return (nq * G + R - 1) / R; };
     auto blocks_of = [&](int n) { return max((n + kKvqBlock - 1) / kKvqBlock, 1); };
-    auto items_of = [&](int b) -> long long {
+    auto items_of = [&](int b) {
         if (b >= p.c.B) return 0;
         int nq, n;
         counts(b, &nq, &n);
-        return (long long)Hkv * tiles_of(nq) * blocks_of(n);
+        return Hkv * tiles_of(nq) * (blocks_of(n) + kUnitCost);
     };
-    // all items, and this CTA's run [lo, hi) of them
-    long long total = 0;
-    for (int b = tid; b < p.c.B; b += kThreads) total += items_of(b);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) sm.scan[warp] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += sm.scan[w];
-    const long long ctas = min((long long)gridDim.x, (total + kMinItems - 1) / kMinItems);
-    if (blockIdx.x >= ctas) return;
-    long long lo = blockIdx.x * total / ctas;
-    const long long hi = (blockIdx.x + 1) * total / ctas;
-    // the sequence that holds item lo
-    int b = 0;
-    long long base = 0;
-    for (int b0 = 0;; b0 += kThreads) {
-        const long long mine = items_of(b0 + tid);
-        long long inc = mine;
+    // Scan of the sequences' items, kThreads at a time: this thread's count and all before it in the
+    // chunk; returns the chunk's sum.  (All items together are below 2^31: checked on the host.)
+    auto scan = [&](int b0, int* mine, int* before) {
+        *mine = items_of(b0 + tid);
+        int inc = *mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += v;
         }
         __syncthreads();
         if (lane == 31) sm.scan[warp] = inc;
-        if (tid == 0) sm.found[0] = -1;
         __syncthreads();
-        long long before = base;
+        *before = inc - *mine;
+        int sum = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            if (w < warp) before += sm.scan[w];
-        if (lo >= before + inc - mine && lo < before + inc) {
-            sm.found[0] = b0 + tid;
-            sm.found[1] = (int)(lo - (before + inc - mine));
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) *before += sm.scan[w];
+            sum += sm.scan[w];
         }
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) base += sm.scan[w];
-        __syncthreads();
-        if (sm.found[0] >= 0) break;
+        return sum;
+    };
+    // all items, and this CTA's run [lo, hi) of them: the first `rest` CTAs take one more
+    int mine, before, chunk = scan(0, &mine, &before), total = chunk, other, skip;
+    for (int b0 = kThreads; b0 < p.c.B; b0 += kThreads) total += scan(b0, &other, &skip);
+    const int ctas = min((int)gridDim.x, (total + kMinItems - 1) / kMinItems), cta = blockIdx.x;
+    if (cta >= ctas) return;
+    const int per = total / ctas, rest = total - per * ctas;
+    const int lo = cta * per + min(cta, rest), hi = lo + per + (cta < rest ? 1 : 0);
+    auto cta_of = [&](int item) {
+        const int edge = rest * (per + 1);
+        return item < edge ? item / (per + 1) : rest + (item - edge) / per;
+    };
+    // the sequence that holds item lo
+    int base = 0, b0 = 0;
+    while (lo >= base + chunk) {
+        base += chunk;
+        b0 += kThreads;
+        chunk = scan(b0, &mine, &before);
     }
-    b = sm.found[0];
-    int off = sm.found[1];
+    if (lo >= base + before && lo < base + before + mine) {
+        sm.found[0] = b0 + tid;
+        sm.found[1] = lo - base - before;
+    }
+    __syncthreads();
 
-    while (lo < hi) {
-        int nq, n;
-        counts(b, &nq, &n);
-        const int nt_ = tiles_of(nq), nb = blocks_of(n), units = Hkv * nt_;
-        const int u = off / nb, k0 = off - u * nb;
-        if (u >= units) {                                // the next sequence with anything to do
-            ++b;
-            off = 0;
-            continue;
-        }
-        const int h = u / nt_, rt = u - h * nt_;
-        const int k1 = (int)min((long long)nb, k0 + (hi - lo));
-        const long long g0 = lo - k0;                    // the unit's first item
-        const int c_lo = (int)(((g0 + 1) * ctas - 1) / total), c_hi = (int)(((g0 + nb) * ctas - 1) / total);
-
-        // queries of the tile: 8 threads a row
-        __syncthreads();
-        if (tid < 8 * R) {
-            const int row = tid >> 3, part = tid & 7, gr = rt * R + row, i = gr / G, gg = gr - i * G;
-            constexpr int E = DH / 8;
-            float x[E];
-            const bool ok = i < nq;
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = 0.f;
-            if (ok) {
-                const T* src = static_cast<const T*>(p.q) + (((size_t)b * p.Tq + i) * p.H + h * G + gg) * DH + part * E;
-#pragma unroll
-                for (int e = 0; e < E; e += Vec16<T>::N) Vec16<T>::ld(src + e, x + e);
+    // A segment: the run's part in one unit (sequence b, KV head h, row tile rt): blocks k0 .. k1 - 1
+    // of nb (none where the run ends within the unit's cost), `len` items; c_lo .. c_hi: the CTAs
+    // with blocks of the unit.
+    struct Segment {
+        int b, h, rt, nq, n, nb, k0, k1, c_lo, c_hi, off, len;
+    };
+    // the segment that starts with item `at`, item `off` of sequence b
+    auto segment = [&](int at, int b, int off) {
+        Segment s;
+        int pos;
+        for (;; ++b, off = 0) {
+            counts(b, &s.nq, &s.n);
+            s.nb = blocks_of(s.n);
+            const int tiles = tiles_of(s.nq), u = off / (s.nb + kUnitCost);
+            if (u < Hkv * tiles) {                       // (else: the next sequence with anything to do)
+                s.h = u / tiles;
+                s.rt = u - s.h * tiles;
+                pos = off - u * (s.nb + kUnitCost);
+                break;
             }
+        }
+        s.b = b;
+        s.off = off;
+        s.len = min(s.nb + kUnitCost - pos, hi - at);
+        s.k0 = max(pos - kUnitCost, 0);
+        s.k1 = pos + s.len - kUnitCost;
+        s.c_lo = cta_of(at - pos + kUnitCost);
+        s.c_hi = cta_of(at - pos + kUnitCost + s.nb - 1);
+        return s;
+    };
+    Walk<T, DH, NT, E4M3> walk(p, sm);
+    // Queries of a tile: 8 threads a row, fetched before the segment's copies are started so that
+    // they need not queue behind them.
+    constexpr int E = DH / 8, QV = E / Vec16<T>::N;
+    uint4 qraw[QV];
+    auto start = [&](const Segment& s) {
+        const int gr = s.rt * R + (tid >> 3), i = gr / G, gg = gr - i * G;
+#pragma unroll
+        for (int v = 0; v < QV; ++v) qraw[v] = make_uint4(0, 0, 0, 0);
+        if (tid < 8 * R && i < s.nq) {
+            const T* src = static_cast<const T*>(p.q) + (((size_t)s.b * p.Tq + i) * p.H + s.h * G + gg) * DH + (tid & 7) * E;
+#pragma unroll
+            for (int v = 0; v < QV; ++v)
+                asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(qraw[v].x), "=r"(qraw[v].y), "=r"(qraw[v].z), "=r"(qraw[v].w)
+                             : "l"(reinterpret_cast<const uint4*>(src) + v));
+        }
+        const int nfull = s.n / kKvqBlock;
+        walk.begin(s.b, s.h, s.k0 + warp, min(s.k1, nfull), s.k1 == s.nb, s.n);
+    };
+    Segment cur = segment(lo, sm.found[0], sm.found[1]);
+    start(cur);
+    for (int at = lo;;) {
+        const int h = cur.h, rt = cur.rt, nq = cur.nq, n = cur.n, b = cur.b, c_lo = cur.c_lo, c_hi = cur.c_hi;
+        if (tid < 8 * R) {
+            const int row = tid >> 3, part = tid & 7, gr = rt * R + row, i = gr / G;
+            float x[E];
+#pragma unroll
+            for (int v = 0; v < QV; ++v) Vec16<T>::unpack(qraw[v], x + v * Vec16<T>::N);
             float amax = 0.f;
 #pragma unroll
             for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[e]));
@@ -685,30 +742,38 @@ __global__ void __launch_bounds__(kThreads, 3) k_kvq_attend(KvqAttendParams p) {
             const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
-                const int at = part * E + e;
+                const int to = part * E + e;
                 const float y0 = x[e] * up, y1 = x[e + 1] * up;
                 const uint32_t hq = pack_f16(y0, y1);
-                *reinterpret_cast<uint32_t*>(&sm.q16[0][row][at]) = hq;
+                *reinterpret_cast<uint32_t*>(&sm.q16[0][row][to]) = hq;
                 if constexpr (A::QP == 2) {
                     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hq));
-                    *reinterpret_cast<uint32_t*>(&sm.q16[1][row][at]) = pack_f16(y0 - f.x, y1 - f.y);
+                    *reinterpret_cast<uint32_t*>(&sm.q16[1][row][to]) = pack_f16(y0 - f.x, y1 - f.y);
                 }
                 uint32_t t[A::TP];
                 split_bf16<A::TP>(x[e], x[e + 1], t);
 #pragma unroll
-                for (int j = 0; j < A::TP; ++j) *reinterpret_cast<uint32_t*>(&sm.qb[j][row][at]) = t[j];
+                for (int j = 0; j < A::TP; ++j) *reinterpret_cast<uint32_t*>(&sm.qb[j][row][to]) = t[j];
             }
             if (part == 0) {
                 sm.qf[row] = p.scale * __uint_as_float((uint32_t)(127 - ex) << 23);
-                sm.lim[row] = ok ? min(n - nq + i, n - 1) : INT32_MAX;      // (a row past the last query: anything)
+                sm.lim[row] = i < nq ? min(n - nq + i, n - 1) : INT32_MAX;  // (a row past the last query: anything)
             }
         }
         __syncthreads();
         State<DH, NT> st;
         init_state<DH, NT>(st);
-        if (n > 0) walk<T, DH, NT, E4M3>(p, sm, st, b, h, n, k0 + warp, k1);
+        walk.run(st);
+        // the next segment's copies run while this one is merged
+        at += cur.len;
+        bool more = at < hi;
+        if (more) {
+            cur = segment(at, b, cur.off + cur.len);
+            more = cur.k1 > cur.k0;
+            if (more) start(cur);
+        }
 
-        // merge the warps: statistics and O through shared memory (the copies' ring is free)
+        // merge the warps: statistics, then O, one warp after the other
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -722,18 +787,40 @@ __global__ void __launch_bounds__(kThreads, 3) k_kvq_attend(KvqAttendParams p) {
                 }
             }
         __syncthreads();
-        float* buf = reinterpret_cast<float*>(sm.ring[0]) + warp * R * DH;   // [row][element]
-        static_assert(kWarps * R * DH * 4 <= kWarps * kRingBytes, "the warps' outputs fit the ring");
-#pragma unroll
-        for (int i = 0; i < A::NM; ++i)
+        {
+            float f[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    *reinterpret_cast<float2*>(buf + (8 * nt + 2 * c + e) * DH + 64 * (i >> 2) + 8 * r + 2 * (i & 3)) =
-                        make_float2(st.o[i][nt][e], st.o[i][nt][e + 2]);
-        __syncthreads();
-        const float* all = reinterpret_cast<const float*>(sm.ring[0]);
+                for (int e = 0; e < 2; ++e) {
+                    float M = sm.m[0][8 * nt + 2 * c + e];
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm.m[w][8 * nt + 2 * c + e]);
+                    f[nt][e] = ex2((st.m[nt][e] - (M == -INFINITY ? 0.f : M)) * kLog2e);
+                }
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (warp == w) {
+#pragma unroll
+                    for (int i = 0; i < A::NM; ++i)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float2* to = reinterpret_cast<float2*>(
+                                    &sm.o[8 * nt + 2 * c + e][o_place(2 * c, 64 * (i >> 2) + 8 * r + 2 * (i & 3))]);
+                                float2 v = make_float2(st.o[i][nt][e] * f[nt][e], st.o[i][nt][e + 2] * f[nt][e]);
+                                if (w > 0) {
+                                    const float2 u = *to;
+                                    v.x += u.x;
+                                    v.y += u.y;
+                                }
+                                *to = v;
+                            }
+                }
+                __syncthreads();
+            }
+        }
         const int rows = min(R, nq * G - rt * R);
         auto put_out = [&](int row, int d4, float4 o, float M, float L) {
             const int gr = rt * R + row, i = gr / G, head = h * G + gr - i * G;
@@ -754,76 +841,102 @@ __global__ void __launch_bounds__(kThreads, 3) k_kvq_attend(KvqAttendParams p) {
                 p.lse[((size_t)b * p.H + head) * p.Tq + i] = L != 0.f ? M + (logf(L) - kPShift * 0.6931471805599453f) : -INFINITY;
         };
         const bool whole = c_lo == c_hi;
-        const int slot = 2 * blockIdx.x + ((int)blockIdx.x == c_lo ? 1 : 0);
-        float* mine = p.part + (size_t)slot * R * (DH + 2);
+        const int slot = 2 * cta + (cta == c_lo ? 1 : 0);
+        float* to = p.part + (size_t)slot * R * (DH + 2);
         for (int e = tid; e < rows * (DH / 4); e += kThreads) {
             const int row = e / (DH / 4), d4 = (e % (DH / 4)) * 4;
-            float M = -INFINITY;
+            float M = -INFINITY, L = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][row]);
             const float ms = M == -INFINITY ? 0.f : M;
-            float4 o = make_float4(0, 0, 0, 0);
-            float L = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2((sm.m[w][row] - ms) * kLog2e);
-                const float4 v = *reinterpret_cast<const float4*>(all + (w * R + row) * DH + d4);
-                o.x = fmaf(v.x, f, o.x);
-                o.y = fmaf(v.y, f, o.y);
-                o.z = fmaf(v.z, f, o.z);
-                o.w = fmaf(v.w, f, o.w);
-                L = fmaf(sm.l[w][row], f, L);
-            }
+            for (int w = 0; w < kWarps; ++w) L = fmaf(sm.l[w][row], ex2((sm.m[w][row] - ms) * kLog2e), L);
+            const float2 o0 = *reinterpret_cast<const float2*>(&sm.o[row][o_place(row, d4)]);
+            const float2 o1 = *reinterpret_cast<const float2*>(&sm.o[row][o_place(row, d4 + 2)]);
+            const float4 o = make_float4(o0.x, o0.y, o1.x, o1.y);
             if (whole) {
                 put_out(row, d4, o, M, L);
             } else {
-                *reinterpret_cast<float4*>(mine + 2 * R + row * DH + d4) = o;
+                __stcg(reinterpret_cast<float4*>(to + 2 * R + row * DH + d4), o);
                 if (d4 == 0) {
-                    mine[row] = M;
-                    mine[R + row] = L;
+                    __stcg(to + row, M);
+                    __stcg(to + R + row, L);
                 }
             }
         }
+        __syncthreads();                                 // (sm.m, sm.l and sm.o are free again, the part is written)
         if (!whole) {
-            __threadfence();
-            __syncthreads();
             if (tid == 0) {
                 unsigned* cnt = p.cnt + ((size_t)b * Hkv + h) * p.RT + rt;
-                const unsigned at = atomicAdd(cnt, 1u);
-                sm.last = at == (unsigned)(c_hi - c_lo);
-                if (at > (unsigned)(c_hi - c_lo)) raise_status(UA_ERR_INVALID_ARG);   // not zeroed
+                __threadfence();
+                const unsigned at_ = atomicAdd(cnt, 1u);
+                sm.last = at_ == (unsigned)(c_hi - c_lo);
+                if (at_ > (unsigned)(c_hi - c_lo)) raise_status(UA_ERR_INVALID_ARG);  // not zeroed
                 if (sm.last) *cnt = 0;
                 __threadfence();
             }
             __syncthreads();
             if (sm.last) {
-                // runs c_lo .. c_hi hold the unit's parts: c_lo in its second slot, the others in their first
+                // CTAs c_lo .. c_hi hold the unit's parts: c_lo in its second slot, the others in their
+                // first.  A thread sums four elements of a row over its share of the parts with a running
+                // maximum (one round of loads), and the shares are joined in order.
                 const size_t ps = (size_t)R * (DH + 2);
-                auto part = [&](int cc) { return p.part + (size_t)(2 * cc + (cc == c_lo ? 1 : 0)) * ps; };
-                for (int e = tid; e < rows * (DH / 4); e += kThreads) {
+                const int parts = c_hi - c_lo + 1;
+                auto part = [&](int i) { return p.part + (size_t)(2 * (c_lo + i) + (i == 0 ? 1 : 0)) * ps; };
+                const int cols = rows * (DH / 4), groups = max(1, min(kThreads / cols, parts));
+                float4* share_o = reinterpret_cast<float4*>(&sm.o[0][0]);
+                float2* share_ml = reinterpret_cast<float2*>(&sm.q16[0][0][0]);      // (the queries have been used)
+                static_assert(sizeof(sm.o) >= kThreads * 16 && sizeof(sm.q16) >= kThreads * 8, "a share for each thread");
+                for (int e0 = 0; e0 < cols; e0 += kThreads) {
+                    const int grp = groups > 1 ? tid / cols : 0, e = e0 + tid - grp * cols;
                     const int row = e / (DH / 4), d4 = (e % (DH / 4)) * 4;
-                    float M = -INFINITY;
-                    for (int cc = c_lo; cc <= c_hi; ++cc) M = fmaxf(M, __ldcg(part(cc) + row));
-                    const float ms = M == -INFINITY ? 0.f : M;
+                    const bool on = e < cols && grp < groups;
+                    float M = -INFINITY, L = 0.f;
                     float4 o = make_float4(0, 0, 0, 0);
-                    float L = 0.f;
-#pragma unroll 4
-                    for (int cc = c_lo; cc <= c_hi; ++cc) {
-                        const float* q = part(cc);
-                        const float f = ex2((__ldcg(q + row) - ms) * kLog2e);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(q + 2 * R + row * DH + d4));
-                        o.x = fmaf(v.x, f, o.x);
-                        o.y = fmaf(v.y, f, o.y);
-                        o.z = fmaf(v.z, f, o.z);
-                        o.w = fmaf(v.w, f, o.w);
-                        L = fmaf(__ldcg(q + R + row), f, L);
+                    auto join = [&](float m, float l, float4 v) {
+                        const float mn = fmaxf(M, m), ms = mn == -INFINITY ? 0.f : mn;
+                        const float f = ex2((M - ms) * kLog2e), g = ex2((m - ms) * kLog2e);
+                        M = mn;
+                        L = fmaf(L, f, l * g);
+                        o.x = fmaf(o.x, f, v.x * g);
+                        o.y = fmaf(o.y, f, v.y * g);
+                        o.z = fmaf(o.z, f, v.z * g);
+                        o.w = fmaf(o.w, f, v.w * g);
+                    };
+                    if (on) {
+                        for (int i = grp; i < parts; i += 4 * groups) {
+                            float m[4], l[4];
+                            float4 v[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const bool in = i + k * groups < parts;
+                                const float* q = part(in ? i + k * groups : i);
+                                m[k] = in ? __ldcg(q + row) : -INFINITY;
+                                l[k] = in ? __ldcg(q + R + row) : 0.f;
+                                v[k] = in ? __ldcg(reinterpret_cast<const float4*>(q + 2 * R + row * DH + d4))
+                                          : make_float4(0, 0, 0, 0);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) join(m[k], l[k], v[k]);
+                        }
                     }
-                    put_out(row, d4, o, M, L);
+                    if (groups > 1) {
+                        if (on) {
+                            share_o[tid] = o;
+                            share_ml[tid] = make_float2(M, L);
+                        }
+                        __syncthreads();
+                        for (int g = 1; on && grp == 0 && g < groups; ++g) {
+                            const float2 ml = share_ml[g * cols + tid];
+                            join(ml.x, ml.y, share_o[g * cols + tid]);
+                        }
+                    }
+                    if (on && grp == 0) put_out(row, d4, o, M, L);
                 }
             }
         }
-        lo += k1 - k0;
-        off += k1 - k0;
+        if (!more) break;
+        __syncthreads();
     }
 }
 

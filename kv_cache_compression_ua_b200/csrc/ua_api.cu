@@ -289,6 +289,9 @@ size_t kvq_ws_bytes(const ua_kvq* c, int H, int Tq) {
 ua_status check_kvq_heads(const ua_kvq* c, int H, int Tq) {
     if (H < 1 || H % c->Hkv != 0 || Tq < 1) return UA_ERR_INVALID_ARG;
     if ((long long)H * c->d > INT32_MAX || (long long)Tq * (H / c->Hkv) > INT32_MAX / 2) return UA_ERR_UNSUPPORTED;
+    // the kernel counts blocks of all sequences, heads and row tiles in 32 bits
+    const double items = (double)c->B * c->Hkv * kvq_row_tiles(c, H, Tq) * ((c->capacity + kKvqBlock - 1) / kKvqBlock);
+    if (items >= (double)INT32_MAX) return UA_ERR_UNSUPPORTED;
     return UA_OK;
 }
 
@@ -1038,10 +1041,10 @@ ua_status ua_kvq_attend(const ua_kvq* c, int H, int Tq, const void* q, const voi
     if (st != UA_OK) return st;
     if ((st = check_kvq_heads(c, H, Tq)) != UA_OK) return st;
     if (!q || !o || !ws || !isfinite(scale)) return UA_ERR_INVALID_ARG;
-    const void* ps[] = {q, g, o};
+    const void* ps[] = {q, g, bias, o};
     for (const void* x : ps)
         if (x && !aligned(x, 16)) return UA_ERR_ALIGNMENT;
-    const void* ws4[] = {bias, n_q, lse};
+    const void* ws4[] = {n_q, lse};
     for (const void* x : ws4)
         if (x && !aligned(x, 4)) return UA_ERR_ALIGNMENT;
     if (!aligned(ws, 256)) return UA_ERR_ALIGNMENT;

@@ -129,9 +129,9 @@ def test_attend_refused(lib):
     assert attend(lib, c, H=1 << 26) == UNSUPPORTED and attend(lib, c, Tq=1 << 30) == UNSUPPORTED
     for kw in (dict(q=None), dict(o=None), dict(ws=None), dict(scale=float("inf")), dict(scale=float("nan"))):
         assert attend(lib, c, **kw) == INVALID
-    for n in ("q", "g", "o", "ws"):
+    for n in ("q", "g", "bias", "o", "ws"):
         assert attend(lib, c, **{n: FAKE + 8}) == ALIGN
-    for n in ("bias", "n_q", "lse"):
+    for n in ("n_q", "lse"):
         assert attend(lib, c, **{n: FAKE + 2}) == ALIGN
     n = S(0)
     assert lib.ua_kvq_attend_workspace_size(ctypes.byref(c), 4, 3, ctypes.byref(n)) == OK
