@@ -26,6 +26,8 @@
 // to arrive, in the order of the runs.
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "tc_common.cuh"
 #include "ua_kernels.h"
 #include "ua_profile.h"
@@ -36,10 +38,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 14.f;             // probabilities are held as 2^14 p
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kRingBytes = 16384;           // per warp
 constexpr int kUnitCost = 6;                // what starting and merging a unit costs, in blocks
-constexpr int kMinItems = 10;               // fewest items (blocks and unit costs) a CTA is given
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -137,6 +137,11 @@ template <typename T, int DH, int NT, bool E4M3> struct Att {
     static constexpr int KB = 64 * DH;               // bytes of a block's keys
     static constexpr int QS = DH + 4;                // row stride of the queries in shared memory
     static constexpr int NM = DH / 16;               // 16-element tiles of the output
+    // One CTA an SM, of as many warps as its registers allow (168 or 255 a thread): few CTAs make few
+    // parts to merge.
+    static constexpr int kWarps = NT == 1 ? 12 : 8, kThreads = 32 * kWarps;
+    static constexpr int kBufs = kWarps / 4;         // buffers the warps' O are added up in
+    static constexpr int kMinItems = kWarps + kUnitCost;    // fewest items (blocks and unit costs) of a run
     struct Smem {
         alignas(128) unsigned char ring[kWarps][kRingBytes];
         alignas(16) float bias[kWarps][NSTG][kKvqBlock];
@@ -145,13 +150,12 @@ template <typename T, int DH, int NT, bool E4M3> struct Att {
         float qf[R];                                 // logit scale times the row's power of two
         int lim[R];                                  // last slot the row sees, -1: none
         float m[kWarps][R], l[kWarps][R];
-        alignas(16) float o[R][DH];                  // the CTA's sum of O, see o_place
-        int scan[kWarps];
-        int found[2];
+        alignas(16) float o[kBufs][R][DH];           // sums of the warps' O, see o_place
+        float2 share[kThreads];
+        int scan[2][kWarps];
         int last;
     };
-    // CTAs an SM holds at once (228 KB of shared memory, 1 KB of each CTA's reserved)
-    static constexpr int CTAS = 3 * (sizeof(Smem) + 1024) <= 228 * 1024 ? 3 : 2;
+    static_assert(sizeof(Smem) <= 227 * 1024, "one CTA an SM");
 };
 
 // What a warp carries through a unit: O^T (elements 64 * pass + 8r + 2mt + {0, 1} of columns
@@ -335,6 +339,7 @@ __device__ __forceinline__ void tail_part(const KvqAttendParams& p, typename Att
 template <typename T, int DH, int NT, bool E4M3> struct Walk {
     using A = Att<T, DH, NT, E4M3>;
     static constexpr long long kNone = -1, kTail = -2, kNoPage = -3;
+    static constexpr int kWarps = A::kWarps;
     static_assert(16 * DH * sizeof(T) <= A::KB, "a warp's rows of the unfinished block fit a block's place");
     const KvqAttendParams& p;
     typename A::Smem& sm;
@@ -400,8 +405,8 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
         first = first_;
         n = n_;
         full = max(0, (last_ - first + kWarps - 1) / kWarps);
-        slot0 = n / kKvqBlock * kKvqBlock + 16 * warp;
-        steps = full + (with_tail && slot0 < n ? 1 : 0);
+        slot0 = n / kKvqBlock * kKvqBlock + 16 * (kWarps - 1 - warp);   // (the last warps have fewer blocks)
+        steps = full + (with_tail && warp >= kWarps - 4 && slot0 < n ? 1 : 0);
         unit = (long long)b * p.c.Hkv + h;
         hrow = (long long)h * p.c.bpp;
         bias0 = p.bias ? p.bias + unit * p.c.cap : nullptr;
@@ -599,9 +604,9 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
 };
 
 template <typename T, int DH, int NT, bool E4M3>
-__global__ void __launch_bounds__(kThreads, Att<T, DH, NT, E4M3>::CTAS) k_kvq_attend(KvqAttendParams p) {
+__global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_attend(KvqAttendParams p) {
     using A = Att<T, DH, NT, E4M3>;
-    constexpr int R = A::R;
+    constexpr int R = A::R, kWarps = A::kWarps, kThreads = A::kThreads;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     typename A::Smem& sm = *reinterpret_cast<typename A::Smem*>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
@@ -619,66 +624,53 @@ __global__ void __launch_bounds__(kThreads, Att<T, DH, NT, E4M3>::CTAS) k_kvq_at
     };
     auto tiles_of = [&](int nq) { return (nq * G + R - 1) / R; };
     auto blocks_of = [&](int n) { return max((n + kKvqBlock - 1) / kKvqBlock, 1); };
-    auto items_of = [&](int b) {
+    auto items_of = [&](int b, int* units) {
+        *units = 0;
         if (b >= p.c.B) return 0;
         int nq, n;
         counts(b, &nq, &n);
-        return Hkv * tiles_of(nq) * (blocks_of(n) + kUnitCost);
+        *units = Hkv * tiles_of(nq);
+        return *units * (blocks_of(n) + kUnitCost);
     };
-    // Scan of the sequences' items, kThreads at a time: this thread's count and all before it in the
-    // chunk; returns the chunk's sum.  (All items together are below 2^31: checked on the host.)
-    auto scan = [&](int b0, int* mine, int* before) {
-        *mine = items_of(b0 + tid);
-        int inc = *mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        __syncthreads();
-        if (lane == 31) sm.scan[warp] = inc;
-        __syncthreads();
-        *before = inc - *mine;
-        int sum = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) *before += sm.scan[w];
-            sum += sm.scan[w];
-        }
-        return sum;
-    };
-    // all items, and this CTA's run [lo, hi) of them: the first `rest` CTAs take one more
-    int mine, before, chunk = scan(0, &mine, &before), total = chunk, other, skip;
-    for (int b0 = kThreads; b0 < p.c.B; b0 += kThreads) total += scan(b0, &other, &skip);
-    const int ctas = min((int)gridDim.x, (total + kMinItems - 1) / kMinItems), cta = blockIdx.x;
-    if (cta >= ctas) return;
-    const int per = total / ctas, rest = total - per * ctas;
-    const int lo = cta * per + min(cta, rest), hi = lo + per + (cta < rest ? 1 : 0);
-    auto cta_of = [&](int item) {
-        const int edge = rest * (per + 1);
-        return item < edge ? item / (per + 1) : rest + (item - edge) / per;
-    };
-    // the sequence that holds item lo
-    int base = 0, b0 = 0;
-    while (lo >= base + chunk) {
-        base += chunk;
-        b0 += kThreads;
-        chunk = scan(b0, &mine, &before);
+    // all items and units (below 2^31: checked on the host)
+    int total = 0, units = 0;
+    for (int b = tid; b < p.c.B; b += kThreads) {
+        int u;
+        total += items_of(b, &u);
+        units += u;
     }
-    if (lo >= base + before && lo < base + before + mine) {
-        sm.found[0] = b0 + tid;
-        sm.found[1] = lo - base - before;
+    total = __reduce_add_sync(0xffffffffu, total);
+    units = __reduce_add_sync(0xffffffffu, units);
+    if (lane == 0) {
+        sm.scan[0][warp] = total;
+        sm.scan[1][warp] = units;
     }
     __syncthreads();
+    total = units = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        total += sm.scan[0][w];
+        units += sm.scan[1][w];
+    }
+    // Equal runs of items, one a CTA.
+    int ctas = max(min(units, (int)gridDim.x), min((int)gridDim.x, (total + A::kMinItems - 1) / A::kMinItems));
+    if (units > 0 && ctas % units * 4 <= ctas) ctas -= ctas % units;    // units of one length: they start where a run starts
+    const int cta = blockIdx.x;
+    if (cta >= ctas) return;
+    // floor(a * b / c) for products below 2^53 (the quotient's fraction is at least 1 / c off a whole number)
+    auto run_start = [&](int k) { return (int)((double)k * (double)total / (double)ctas); };
+    auto run_of = [&](int item) { return (int)((((double)item + 1.0) * ctas - 1.0) / total); };
 
-    // A segment: the run's part in one unit (sequence b, KV head h, row tile rt): blocks k0 .. k1 - 1
-    // of nb (none where the run ends within the unit's cost), `len` items; c_lo .. c_hi: the CTAs
-    // with blocks of the unit.
+    // A segment: a run's part in one unit (sequence b, KV head h, row tile rt): blocks k0 .. k1 - 1 of
+    // nb (none where the run ends within the unit's cost), `len` items; r_lo .. r_hi: the runs with
+    // blocks of the unit.
     struct Segment {
-        int b, h, rt, nq, n, nb, k0, k1, c_lo, c_hi, off, len;
+        int b, h, rt, nq, n, nb, k0, k1, r_lo, r_hi, off, len;
     };
+    int at = run_start(cta);
+    const int hi = run_start(cta + 1);
     // the segment that starts with item `at`, item `off` of sequence b
-    auto segment = [&](int at, int b, int off) {
+    auto segment = [&](int b, int off) {
         Segment s;
         int pos;
         for (;; ++b, off = 0) {
@@ -697,9 +689,27 @@ __global__ void __launch_bounds__(kThreads, Att<T, DH, NT, E4M3>::CTAS) k_kvq_at
         s.len = min(s.nb + kUnitCost - pos, hi - at);
         s.k0 = max(pos - kUnitCost, 0);
         s.k1 = pos + s.len - kUnitCost;
-        s.c_lo = cta_of(at - pos + kUnitCost);
-        s.c_hi = cta_of(at - pos + kUnitCost + s.nb - 1);
+        s.r_lo = run_of(at - pos + kUnitCost);
+        s.r_hi = run_of(at - pos + kUnitCost + s.nb - 1);
         return s;
+    };
+    // the sequence that holds item `at`, 32 sequences at a time
+    auto find = [&]() {
+        for (int seq = 0, first = 0;; seq += 32) {
+            int u, inc = items_of(seq + lane, &u);
+            const int mine = inc;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, at < first + inc);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                return segment(seq + l, at - first - __shfl_sync(0xffffffffu, inc - mine, l));
+            }
+            first += __shfl_sync(0xffffffffu, inc, 31);
+        }
     };
     Walk<T, DH, NT, E4M3> walk(p, sm);
     // Queries of a tile: 8 threads a row, fetched before the segment's copies are started so that
@@ -721,10 +731,10 @@ __global__ void __launch_bounds__(kThreads, Att<T, DH, NT, E4M3>::CTAS) k_kvq_at
         const int nfull = s.n / kKvqBlock;
         walk.begin(s.b, s.h, s.k0 + warp, min(s.k1, nfull), s.k1 == s.nb, s.n);
     };
-    Segment cur = segment(lo, sm.found[0], sm.found[1]);
+    Segment cur = find();
     start(cur);
-    for (int at = lo;;) {
-        const int h = cur.h, rt = cur.rt, nq = cur.nq, n = cur.n, b = cur.b, c_lo = cur.c_lo, c_hi = cur.c_hi;
+    for (;;) {
+        const int h = cur.h, rt = cur.rt, nq = cur.nq, n = cur.n, b = cur.b, r_lo = cur.r_lo, r_hi = cur.r_hi;
         if (tid < 8 * R) {
             const int row = tid >> 3, part = tid & 7, gr = rt * R + row, i = gr / G;
             float x[E];
@@ -768,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, Att<T, DH, NT, E4M3>::CTAS) k_kvq_at
         at += cur.len;
         bool more = at < hi;
         if (more) {
-            cur = segment(at, b, cur.off + cur.len);
+            cur = segment(b, cur.off + cur.len);
             more = cur.k1 > cur.k0;
             if (more) start(cur);
         }
@@ -798,9 +808,9 @@ __global__ void __launch_bounds__(kThreads, Att<T, DH, NT, E4M3>::CTAS) k_kvq_at
                     for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm.m[w][8 * nt + 2 * c + e]);
                     f[nt][e] = ex2((st.m[nt][e] - (M == -INFINITY ? 0.f : M)) * kLog2e);
                 }
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (warp == w) {
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) {                // buffer j adds up warps j, j + kBufs, ..
+                if (warp / A::kBufs == w) {
 #pragma unroll
                     for (int i = 0; i < A::NM; ++i)
 #pragma unroll
@@ -808,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, Att<T, DH, NT, E4M3>::CTAS) k_kvq_at
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 float2* to = reinterpret_cast<float2*>(
-                                    &sm.o[8 * nt + 2 * c + e][o_place(2 * c, 64 * (i >> 2) + 8 * r + 2 * (i & 3))]);
+                                    &sm.o[warp % A::kBufs][8 * nt + 2 * c + e][o_place(2 * c, 64 * (i >> 2) + 8 * r + 2 * (i & 3))]);
                                 float2 v = make_float2(st.o[i][nt][e] * f[nt][e], st.o[i][nt][e + 2] * f[nt][e]);
                                 if (w > 0) {
                                     const float2 u = *to;
@@ -840,8 +850,8 @@ __global__ void __launch_bounds__(kThreads, Att<T, DH, NT, E4M3>::CTAS) k_kvq_at
             if (p.lse && d4 == 0)
                 p.lse[((size_t)b * p.H + head) * p.Tq + i] = L != 0.f ? M + (logf(L) - kPShift * 0.6931471805599453f) : -INFINITY;
         };
-        const bool whole = c_lo == c_hi;
-        const int slot = 2 * cta + (cta == c_lo ? 1 : 0);
+        const bool whole = r_lo == r_hi;
+        const int slot = 2 * cta + (cta == r_lo ? 1 : 0);
         float* to = p.part + (size_t)slot * R * (DH + 2);
         for (int e = tid; e < rows * (DH / 4); e += kThreads) {
             const int row = e / (DH / 4), d4 = (e % (DH / 4)) * 4;
@@ -851,9 +861,16 @@ __global__ void __launch_bounds__(kThreads, Att<T, DH, NT, E4M3>::CTAS) k_kvq_at
             const float ms = M == -INFINITY ? 0.f : M;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) L = fmaf(sm.l[w][row], ex2((sm.m[w][row] - ms) * kLog2e), L);
-            const float2 o0 = *reinterpret_cast<const float2*>(&sm.o[row][o_place(row, d4)]);
-            const float2 o1 = *reinterpret_cast<const float2*>(&sm.o[row][o_place(row, d4 + 2)]);
-            const float4 o = make_float4(o0.x, o0.y, o1.x, o1.y);
+            float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < A::kBufs; ++j) {
+                const float2 o0 = *reinterpret_cast<const float2*>(&sm.o[j][row][o_place(row, d4)]);
+                const float2 o1 = *reinterpret_cast<const float2*>(&sm.o[j][row][o_place(row, d4 + 2)]);
+                o.x += o0.x;
+                o.y += o0.y;
+                o.z += o1.x;
+                o.w += o1.y;
+            }
             if (whole) {
                 put_out(row, d4, o, M, L);
             } else {
@@ -870,23 +887,23 @@ __global__ void __launch_bounds__(kThreads, Att<T, DH, NT, E4M3>::CTAS) k_kvq_at
                 unsigned* cnt = p.cnt + ((size_t)b * Hkv + h) * p.RT + rt;
                 __threadfence();
                 const unsigned at_ = atomicAdd(cnt, 1u);
-                sm.last = at_ == (unsigned)(c_hi - c_lo);
-                if (at_ > (unsigned)(c_hi - c_lo)) raise_status(UA_ERR_INVALID_ARG);  // not zeroed
+                sm.last = at_ == (unsigned)(r_hi - r_lo);
+                if (at_ > (unsigned)(r_hi - r_lo)) raise_status(UA_ERR_INVALID_ARG);  // not zeroed
                 if (sm.last) *cnt = 0;
                 __threadfence();
             }
             __syncthreads();
             if (sm.last) {
-                // CTAs c_lo .. c_hi hold the unit's parts: c_lo in its second slot, the others in their
+                // Runs r_lo .. r_hi hold the unit's parts: r_lo in its second slot, the others in their
                 // first.  A thread sums four elements of a row over its share of the parts with a running
                 // maximum (one round of loads), and the shares are joined in order.
                 const size_t ps = (size_t)R * (DH + 2);
-                const int parts = c_hi - c_lo + 1;
-                auto part = [&](int i) { return p.part + (size_t)(2 * (c_lo + i) + (i == 0 ? 1 : 0)) * ps; };
+                const int parts = r_hi - r_lo + 1;
+                auto part = [&](int i) { return p.part + (size_t)(2 * (r_lo + i) + (i == 0 ? 1 : 0)) * ps; };
                 const int cols = rows * (DH / 4), groups = max(1, min(kThreads / cols, parts));
-                float4* share_o = reinterpret_cast<float4*>(&sm.o[0][0]);
-                float2* share_ml = reinterpret_cast<float2*>(&sm.q16[0][0][0]);      // (the queries have been used)
-                static_assert(sizeof(sm.o) >= kThreads * 16 && sizeof(sm.q16) >= kThreads * 8, "a share for each thread");
+                float4* share_o = reinterpret_cast<float4*>(&sm.o[0][0][0]);
+                float2* share_ml = sm.share;
+                static_assert(sizeof(sm.o) >= kThreads * 16, "a share for each thread");
                 for (int e0 = 0; e0 < cols; e0 += kThreads) {
                     const int grp = groups > 1 ? tid / cols : 0, e = e0 + tid - grp * cols;
                     const int row = e / (DH / 4), d4 = (e % (DH / 4)) * 4;
@@ -943,12 +960,12 @@ __global__ void __launch_bounds__(kThreads, Att<T, DH, NT, E4M3>::CTAS) k_kvq_at
 template <typename T, int DH, int NT, bool E4M3> cudaError_t attend(const KvqAttendParams& p, cudaStream_t s) {
     using A = Att<T, DH, NT, E4M3>;
     auto kern = k_kvq_attend<T, DH, NT, E4M3>;
-    const int smem = (int)sizeof(typename A::Smem);
+    const int smem = (int)sizeof(typename A::Smem), kThreads = A::kThreads;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // at most the blocks of full caches: the lengths are known on the device only
     const long long most = (long long)p.c.B * p.c.Hkv * p.RT * ((p.c.cap + kKvqBlock - 1) / kKvqBlock);
-    const long long want = (most + kMinItems - 1) / kMinItems;
+    const long long want = std::max(most * (1 + kUnitCost) / A::kMinItems, (long long)p.c.B * p.c.Hkv * p.RT) + 1;
     UA_PROFILE("k_kvq_attend", s);
     return launch_dependent(kern, dim3((unsigned)(want < kKvqAttendCtas ? want : kKvqAttendCtas)), dim3(kThreads),
                             (size_t)smem, s, p);

@@ -290,7 +290,8 @@ ua_status check_kvq_heads(const ua_kvq* c, int H, int Tq) {
     if (H < 1 || H % c->Hkv != 0 || Tq < 1) return UA_ERR_INVALID_ARG;
     if ((long long)H * c->d > INT32_MAX || (long long)Tq * (H / c->Hkv) > INT32_MAX / 2) return UA_ERR_UNSUPPORTED;
     // the kernel counts blocks of all sequences, heads and row tiles in 32 bits
-    const double items = (double)c->B * c->Hkv * kvq_row_tiles(c, H, Tq) * ((c->capacity + kKvqBlock - 1) / kKvqBlock);
+    // (with a few items more for each unit, see kUnitCost)
+    const double items = (double)c->B * c->Hkv * kvq_row_tiles(c, H, Tq) * ((c->capacity + kKvqBlock - 1) / kKvqBlock + 16);
     if (items >= (double)INT32_MAX) return UA_ERR_UNSUPPORTED;
     return UA_OK;
 }

@@ -424,7 +424,7 @@ struct KvqAttendParams {
     unsigned* cnt;                 // [B * Hkv * RT] arrivals, zero between calls
     float* part;                   // [CTAs][2][rows][d + 2] partial states
 };
-constexpr int kKvqAttendCtas = 148 * 3;   // most CTAs of the attention (slots of `part`)
+constexpr int kKvqAttendCtas = 148;       // most CTAs of the attention (slots of `part`)
 inline int kvq_row_tile(int rows) { return rows <= 8 ? 8 : 16; }
 cudaError_t launch_kvq_attend(const KvqAttendParams& p, int d, bool bf16, bool e4m3, cudaStream_t s);
 
