@@ -36,7 +36,11 @@ namespace ua {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+// Logits are held in units of ln 4, so that the lowest finite bias still fits; the running maximum of a
+// column is a whole number of them (at or above its logits), so every rescale is a power of two and
+// the shift below is exact.
+constexpr float kLog4e = 0.72134752044448170f;
+constexpr float kLn4 = 1.3862943611198906f;
 constexpr float kPShift = 14.f;             // probabilities are held as 2^14 p
 constexpr int kRingBytes = 16384;           // per warp
 constexpr int kUnitCost = 6;                // what starting and merging a unit costs, in blocks
@@ -45,6 +49,12 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// d = a b + c, d += a b
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint2 b, const float (&c)[4]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint2 b) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -68,8 +78,9 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Four codes of a word -> two f16x2 (bytes 0,1 and 2,3), exactly.  int8: the byte with its sign
-// flipped is a mantissa of 1024 + (code + 128).
+// Four codes of a word -> two f16x2, exactly.  e4m3: codes 0, 1 and 2, 3.  int8: codes 0, 2 and 1, 3, each
+// as (code + 128) 2^-24: the byte with its sign bit flipped is the mantissa of a subnormal f16, so no
+// arithmetic is needed; the 128 are taken off by what the products' sums start from.
 template <bool E4M3> __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
     if constexpr (E4M3) {
         asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
@@ -77,13 +88,19 @@ template <bool E4M3> __device__ __forceinline__ void codes_f16(uint32_t w, uint3
             : "=r"(lo), "=r"(hi)
             : "r"(w));
     } else {
-        w ^= 0x80808080u;
-        const __half2 off = __half2half2(__ushort_as_half(0x6480));        // 1152
-        uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
-        __half2 ha = __hsub2(*reinterpret_cast<__half2*>(&a), off), hb = __hsub2(*reinterpret_cast<__half2*>(&b), off);
-        lo = *reinterpret_cast<uint32_t*>(&ha);
-        hi = *reinterpret_cast<uint32_t*>(&hb);
+        lo = (w & 0x00ff00ffu) ^ 0x00800080u;
+        hi = ((w >> 8) & 0x00ff00ffu) ^ 0x00800080u;
     }
+}
+// Bytes of two tokens' words so that codes_f16 pairs the tokens: elements 0, 1 (k = 0) or 2, 3 (k = 1)
+// of both.
+template <bool E4M3> __device__ __forceinline__ uint32_t token_pair(uint32_t t0, uint32_t t1, int k) {
+    return __byte_perm(t0, t1, E4M3 ? (k ? 0x7362 : 0x5140) : (k ? 0x7632 : 0x5410));
+}
+constexpr float kI8Unit = 5.9604644775390625e-8f;       // 2^-24
+// Place of a query's element among its four neighbours, as codes_f16 orders a key's.
+template <bool E4M3> __device__ __forceinline__ constexpr int q_order(int e) {
+    return E4M3 ? e : (e & ~3) | ((e & 1) << 1) | ((e >> 1) & 1);
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
@@ -147,7 +164,8 @@ template <typename T, int DH, int NT, bool E4M3> struct Att {
         alignas(16) float bias[kWarps][NSTG][kKvqBlock];
         alignas(16) uint16_t q16[QP][R][QS];         // f16, scaled by a power of two a row
         alignas(16) uint16_t qb[TP][R][QS];          // bf16 parts (for the unfinished block)
-        float qf[R];                                 // logit scale times the row's power of two
+        float qf[R];                                 // logit scale in ln 4 times the row's power of two
+        float s0[R];                                 // -128 * sum of the row's f16 values (int8, see codes_f16)
         int lim[R];                                  // last slot the row sees, -1: none
         float m[kWarps][R], l[kWarps][R];
         alignas(16) float o[kBufs][R][DH];           // sums of the warps' O, see o_place
@@ -167,6 +185,7 @@ template <int DH, int NT> struct State {
 
 // Online softmax of 16 * MT tokens: logits x[mt][nt][e] (rows: tokens tok_of(r) and + 8, columns as
 // in State) -> 2^14 p in place, corr = factor of what was accumulated, any: whether the column sees one.
+// The sums are left to the caller.
 template <int DH, int NT, int MT>
 __device__ __forceinline__ void block_softmax(State<DH, NT>& st, float (&x)[MT][NT][4], float (&corr)[NT][2],
                                               bool (&any)[NT][2]) {
@@ -181,20 +200,17 @@ __device__ __forceinline__ void block_softmax(State<DH, NT>& st, float (&x)[MT][
             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             // (a NaN logit is no maximum; it makes the sum NaN, and with it every output of the row)
             any[nt][e] = mx > -INFINITY;
-            const float mn = fmaxf(st.m[nt][e], mx);
+            const float mn = fmaxf(st.m[nt][e], ceilf(mx));
             const float ms = mn == -INFINITY ? 0.f : mn;
-            corr[nt][e] = ex2((st.m[nt][e] - ms) * kLog2e);
+            corr[nt][e] = ex2(2.f * (st.m[nt][e] - ms));
             st.m[nt][e] = mn;
-            float sum = 0.f;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     float& v = x[mt][nt][e + 2 * k];
-                    v = ex2(fmaf(v - ms, kLog2e, kPShift));   // (v - ms first: exact 0 at the lowest float)
-                    sum += v;
+                    v = ex2(fmaf(v - ms, 2.f, kPShift));
                 }
-            st.l[nt][e] = fmaf(st.l[nt][e], corr[nt][e], sum);
         }
 }
 
@@ -275,12 +291,17 @@ __device__ __forceinline__ void tail_part(const KvqAttendParams& p, typename Att
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float& v = x[0][nt][2 * k + e];
-                v = hidden[k] || slot0 + tok_of(r) + 8 * k > sm.lim[8 * nt + 2 * c + e] ? -INFINITY
-                                                                                       : fmaf(v, p.scale, bs[k]);
+                v = hidden[k] || slot0 + tok_of(r) + 8 * k > sm.lim[8 * nt + 2 * c + e]
+                        ? -INFINITY
+                        : fmaf(v, p.scale * kLog4e, bs[k] * kLog4e);
             }
     float corr[NT][2];
     bool any[NT][2];
     block_softmax<DH, NT, 1>(st, x, corr, any);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) st.l[nt][e] = fmaf(st.l[nt][e], corr[nt][e], x[0][nt][e] + x[0][nt][e + 2]);
     uint2 pb[A::TPP][NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -421,13 +442,14 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
         vs = rows[0] >= 0 ? __ldg(p.c.vs + rows[0]) : 0.f;
     }
     __device__ __forceinline__ void run(State<DH, NT>& st) {
-        float qf[NT][2];
+        float qf[NT][2], s0[NT][4];                      // s0: what the sums of the products start from
         int lim[NT][2], lim_min = INT32_MAX;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 qf[nt][e] = sm.qf[8 * nt + 2 * c + e];
+                s0[nt][e] = s0[nt][e + 2] = E4M3 ? 0.f : sm.s0[8 * nt + 2 * c + e];
                 lim[nt][e] = sm.lim[8 * nt + 2 * c + e];
                 lim_min = min(lim_min, lim[nt][e]);
             }
@@ -442,7 +464,7 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
             const float ksn = rows[0] >= 0 ? __ldg(p.c.ks + rows[0]) : 0.f;
             const float vsn = rows[0] >= 0 ? __ldg(p.c.vs + rows[0]) : 0.f;
             if (row >= 0) {
-                block(st, i, next, stg, qf, lim, lim_min);
+                block(st, i, next, stg, qf, s0, lim, lim_min);
             } else {
                 if (row == kTail) {                      // the last step
                     cp_async_wait<0>();
@@ -463,7 +485,7 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
         __syncwarp();
     }
     __device__ __forceinline__ void block(State<DH, NT>& st, int i, long long next, int stg, const float (&qf)[NT][2],
-                                          const int (&lim)[NT][2], int lim_min) {
+                                          const float (&s0)[NT][4], const int (&lim)[NT][2], int lim_min) {
         const int blk = first + i * kWarps;
         const unsigned char* kb = sm.ring[warp] + stg * 2 * A::KB;
         const unsigned char* vb = kb + A::KB;
@@ -472,21 +494,15 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
         __syncwarp();
         float x[4][NT][4];
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[mt][nt][e] = 0.f;
-#pragma unroll
         for (int hf = 0; hf < DH / 64; ++hf) {
             uint2 q[A::QP][NT][4];
 #pragma unroll
-            for (int i = 0; i < A::QP; ++i)
+            for (int j = 0; j < A::QP; ++j)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        q[i][nt][s] = *reinterpret_cast<const uint2*>(&sm.q16[i][8 * nt + r][64 * hf + 16 * c + 4 * s]);
+                        q[j][nt][s] = *reinterpret_cast<const uint2*>(&sm.q16[j][8 * nt + r][64 * hf + 16 * c + 4 * s]);
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
                 const int tok = 16 * mt + tok_of(r);
@@ -501,7 +517,10 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int i = 0; i < A::QP; ++i) mma_f16(x[mt][nt], a, q[i][nt][s]);
+                        for (int j = 0; j < A::QP; ++j) {
+                            if (hf + s + j == 0) mma_f16(x[mt][nt], a, q[j][nt][s], s0[nt]);
+                            else mma_f16(x[mt][nt], a, q[j][nt][s]);
+                        }
                 }
             }
         }
@@ -514,27 +533,73 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
         }
         __syncwarp();
         load_k(next, i + A::NSTG, stg);
-        // logits
-        const bool masked = blk * kKvqBlock + kKvqBlock - 1 > lim_min;
+        // Probabilities.  Where every slot is seen and nothing is added to the logits, they are one fused
+        // multiply-add and an exp2 away from the products: the shift 2 m - 14 is checked to be exact.
+        float corr[NT][2], f[NT][2];
+        bool any[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float f = qf[nt][e] * ks;
+            for (int e = 0; e < 2; ++e) f[nt][e] = E4M3 ? qf[nt][e] * ks : qf[nt][e] * ks * (1.f / kI8Unit);
+        bool plain = bias0 == nullptr && blk * kKvqBlock + kKvqBlock - 1 <= lim_min && p.scale > 0.f;
+        if (plain) {
+            float mn[NT][2], base[NT][2];
+            bool exact = true;
 #pragma unroll
-                for (int mt = 0; mt < 4; ++mt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float& v = x[mt][nt][2 * k + e];
-                        v *= f;
-                        if (bias0) v = bs[mt][k] == -INFINITY ? -INFINITY : v + bs[mt][k];
-                        if (masked && blk * kKvqBlock + 16 * mt + tok_of(r) + 8 * k > lim[nt][e]) v = -INFINITY;
+                for (int e = 0; e < 2; ++e) {
+                    float mx = x[0][nt][e];
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt) mx = fmaxf(mx, fmaxf(x[mt][nt][e], x[mt][nt][e + 2]));
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    mn[nt][e] = fmaxf(st.m[nt][e], ceilf(mx * f[nt][e]));
+                    base[nt][e] = 2.f * mn[nt][e] - kPShift;
+                    exact = exact && 2.f * mn[nt][e] - base[nt][e] == kPShift;
+                }
+            plain = __all_sync(0xffffffffu, exact);
+            if (plain) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        any[nt][e] = true;
+                        corr[nt][e] = ex2(2.f * (st.m[nt][e] - mn[nt][e]));
+                        st.m[nt][e] = mn[nt][e];
+                        const float f2 = 2.f * f[nt][e];
+#pragma unroll
+                        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                float& v = x[mt][nt][2 * k + e];
+                                v = ex2(fmaf(v, f2, -base[nt][e]));
+                            }
                     }
             }
-        float corr[NT][2];
-        bool any[NT][2];
-        block_softmax<DH, NT, 4>(st, x, corr, any);
+        }
+        if (!plain) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float& v = x[mt][nt][2 * k + e];
+                            v *= f[nt][e];
+                            if (bias0) v = bs[mt][k] == -INFINITY ? -INFINITY : fmaf(bs[mt][k], kLog4e, v);
+                            if (blk * kKvqBlock + 16 * mt + tok_of(r) + 8 * k > lim[nt][e]) v = -INFINITY;
+                        }
+            block_softmax<DH, NT, 4>(st, x, corr, any);
+        }
+        // P^T as the products' operand; int8 also needs the sums of the rounded values, by a product
+        // with ones
         uint2 pb[A::PP][4][NT];
+        float sum[NT][4];
+        const uint32_t ones[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+        const float none[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -547,7 +612,35 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
                     pb[1][mt][nt] = make_uint2(transpose8x8(pack_f16(x[mt][nt][0] - l2.x, x[mt][nt][1] - l2.y)),
                                                transpose8x8(pack_f16(x[mt][nt][2] - h2.x, x[mt][nt][3] - h2.y)));
                 }
+                if constexpr (!E4M3) {
+                    if (mt == 0) mma_f16(sum[nt], ones, pb[0][mt][nt], none);
+                    else mma_f16(sum[nt], ones, pb[0][mt][nt]);
+                    if constexpr (A::PP == 2) mma_f16(sum[nt], ones, pb[1][mt][nt]);
+                }
             }
+        bool rescale = false;
+        float o0[NT][4], fv[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l = x[0][nt][e] + x[0][nt][e + 2];
+#pragma unroll
+                for (int mt = 1; mt < 4; ++mt) l += x[mt][nt][e] + x[mt][nt][e + 2];
+                st.l[nt][e] = fmaf(st.l[nt][e], corr[nt][e], l);
+                rescale = rescale || corr[nt][e] != 1.f;
+                o0[nt][e] = o0[nt][e + 2] = E4M3 ? 0.f : -128.f * kI8Unit * sum[nt][e];
+                // (a block no slot of which is seen may have a NaN scale)
+                fv[nt][e] = any[nt][e] ? (E4M3 ? vs : vs * (1.f / kI8Unit)) : 0.f;
+            }
+        if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+            for (int k = 0; k < A::NM; ++k)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) st.o[k][nt][e] *= corr[nt][e & 1];
+        }
         // O^T += vs * V^T P^T
         cp_async_wait<2 * A::NSTG - 1>();
         __syncwarp();
@@ -555,17 +648,11 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
         for (int pass = 0; pass < DH / 64; ++pass) {
             float acc[4][NT][4];
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[mt][nt][e] = 0.f;
-#pragma unroll
             for (int kt = 0; kt < 4; ++kt) {
-                uint2 w[4];                          // tokens 4i + c, elements 64 pass + 8r ..
+                uint2 w[4];                              // tokens 4k + c, elements 64 pass + 8r ..
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[i] = *reinterpret_cast<const uint2*>(vb + v_place<DH>(16 * kt + 4 * i + c, 4 * pass + (r >> 1)) +
+                for (int k = 0; k < 4; ++k)
+                    w[k] = *reinterpret_cast<const uint2*>(vb + v_place<DH>(16 * kt + 4 * k + c, 4 * pass + (r >> 1)) +
                                                            8 * (r & 1));
 #pragma unroll
                 for (int hw = 0; hw < 2; ++hw) {
@@ -574,29 +661,25 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         uint32_t a[4];
-                        const uint32_t sel = k ? 0x7362 : 0x5140;
-                        codes_f16<E4M3>(__byte_perm(t0, t1, sel), a[0], a[1]);
-                        codes_f16<E4M3>(__byte_perm(t2, t3, sel), a[2], a[3]);
+                        codes_f16<E4M3>(token_pair<E4M3>(t0, t1, k), a[0], a[1]);
+                        codes_f16<E4M3>(token_pair<E4M3>(t2, t3, k), a[2], a[3]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int i = 0; i < A::PP; ++i) mma_f16(acc[2 * hw + k][nt], a, pb[i][kt][nt]);
+                            for (int j = 0; j < A::PP; ++j) {
+                                if (kt + j == 0) mma_f16(acc[2 * hw + k][nt], a, pb[j][kt][nt], o0[nt]);
+                                else mma_f16(acc[2 * hw + k][nt], a, pb[j][kt][nt]);
+                            }
                     }
                 }
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float f = any[nt][e] ? vs : 0.f;   // (a block no slot of which is seen may have a NaN scale)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            float& o = st.o[4 * pass + mt][nt][2 * k + e];
-                            o = fmaf(acc[mt][nt][2 * k + e], f, o * corr[nt][e]);
-                        }
-                }
+                    for (int e = 0; e < 4; ++e)
+                        st.o[4 * pass + mt][nt][e] = fmaf(acc[mt][nt][e], fv[nt][e & 1], st.o[4 * pass + mt][nt][e]);
         }
         __syncwarp();
         load_v(next, stg);
@@ -752,21 +835,33 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
             const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
-                const int to = part * E + e;
-                const float y0 = x[e] * up, y1 = x[e + 1] * up;
-                const uint32_t hq = pack_f16(y0, y1);
-                *reinterpret_cast<uint32_t*>(&sm.q16[0][row][to]) = hq;
-                if constexpr (A::QP == 2) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hq));
-                    *reinterpret_cast<uint32_t*>(&sm.q16[1][row][to]) = pack_f16(y0 - f.x, y1 - f.y);
-                }
                 uint32_t t[A::TP];
                 split_bf16<A::TP>(x[e], x[e + 1], t);
 #pragma unroll
-                for (int j = 0; j < A::TP; ++j) *reinterpret_cast<uint32_t*>(&sm.qb[j][row][to]) = t[j];
+                for (int j = 0; j < A::TP; ++j) *reinterpret_cast<uint32_t*>(&sm.qb[j][row][part * E + e]) = t[j];
             }
+            float qsum = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; e += 4)
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {         // places k, k + 1 of four
+                    const float y0 = x[e + q_order<E4M3>(k)] * up, y1 = x[e + q_order<E4M3>(k + 1)] * up;
+                    const uint32_t hq = pack_f16(y0, y1);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hq));
+                    *reinterpret_cast<uint32_t*>(&sm.q16[0][row][part * E + e + k]) = hq;
+                    qsum += f.x + f.y;
+                    if constexpr (A::QP == 2) {
+                        const uint32_t lq = pack_f16(y0 - f.x, y1 - f.y);
+                        const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&lq));
+                        *reinterpret_cast<uint32_t*>(&sm.q16[1][row][part * E + e + k]) = lq;
+                        qsum += g.x + g.y;
+                    }
+                }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) qsum += __shfl_xor_sync(mask, qsum, o);
             if (part == 0) {
-                sm.qf[row] = p.scale * __uint_as_float((uint32_t)(127 - ex) << 23);
+                sm.qf[row] = p.scale * kLog4e * __uint_as_float((uint32_t)(127 - ex) << 23);
+                sm.s0[row] = -128.f * kI8Unit * qsum;
                 sm.lim[row] = i < nq ? min(n - nq + i, n - 1) : INT32_MAX;  // (a row past the last query: anything)
             }
         }
@@ -806,7 +901,7 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
                     float M = sm.m[0][8 * nt + 2 * c + e];
 #pragma unroll
                     for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm.m[w][8 * nt + 2 * c + e]);
-                    f[nt][e] = ex2((st.m[nt][e] - (M == -INFINITY ? 0.f : M)) * kLog2e);
+                    f[nt][e] = ex2(2.f * (st.m[nt][e] - (M == -INFINITY ? 0.f : M)));
                 }
 #pragma unroll 1
             for (int w = 0; w < 4; ++w) {                // buffer j adds up warps j, j + kBufs, ..
@@ -848,7 +943,7 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
                 *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
             }
             if (p.lse && d4 == 0)
-                p.lse[((size_t)b * p.H + head) * p.Tq + i] = L != 0.f ? M + (logf(L) - kPShift * 0.6931471805599453f) : -INFINITY;
+                p.lse[((size_t)b * p.H + head) * p.Tq + i] = L != 0.f ? M * kLn4 + (logf(L) - kPShift * 0.6931471805599453f) : -INFINITY;
         };
         const bool whole = r_lo == r_hi;
         const int slot = 2 * cta + (cta == r_lo ? 1 : 0);
@@ -860,7 +955,7 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][row]);
             const float ms = M == -INFINITY ? 0.f : M;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) L = fmaf(sm.l[w][row], ex2((sm.m[w][row] - ms) * kLog2e), L);
+            for (int w = 0; w < kWarps; ++w) L = fmaf(sm.l[w][row], ex2(2.f * (sm.m[w][row] - ms)), L);
             float4 o = make_float4(0, 0, 0, 0);
 #pragma unroll
             for (int j = 0; j < A::kBufs; ++j) {
@@ -912,7 +1007,7 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
                     float4 o = make_float4(0, 0, 0, 0);
                     auto join = [&](float m, float l, float4 v) {
                         const float mn = fmaxf(M, m), ms = mn == -INFINITY ? 0.f : mn;
-                        const float f = ex2((M - ms) * kLog2e), g = ex2((m - ms) * kLog2e);
+                        const float f = ex2(2.f * (M - ms)), g = ex2(2.f * (m - ms));
                         M = mn;
                         L = fmaf(L, f, l * g);
                         o.x = fmaf(o.x, f, v.x * g);

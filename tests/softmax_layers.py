@@ -122,6 +122,18 @@ def rows_of(cache, which, b, h, n):
     return torch.cat(out)
 
 
+def offsets_of(cache, which, b, h, n):
+    """[n, 1]: 128 scales of an int8 slot: its products are formed with code + 128, so the rounding of their sums
+    is relative to |value| + 128 scales.  0 for e4m3 and for rows in the ring."""
+    out = torch.zeros(n, 1, dtype=torch.float64)
+    if cache.k.dtype == torch.int8:
+        sc = cache.k_scale if which == "k" else cache.v_scale
+        for blk in range(n // BLOCK):
+            pg = b if cache.page_table is None else int(cache.page_table[b, blk * BLOCK // cache.page_size])
+            out[blk * BLOCK:(blk + 1) * BLOCK] = 128 * d64(sc[pg, h, blk * BLOCK % cache.page_size // BLOCK])
+    return out
+
+
 def attend(cache, q, n, *, g=None, bias=None, n_q=None, scale=None):
     """o [B,Tq,H,d], its bound, lse [B,H,Tq], its bound, and the rows that are written [B,Tq].
 
@@ -129,7 +141,8 @@ def attend(cache, q, n, *, g=None, bias=None, n_q=None, scale=None):
     sum |q||k| (fp32 queries and keys of three bf16 parts: 2^-22 of it more), the bias 4 of its size and the
     logit's.  A logit off by e moves every probability by a factor within e; probabilities are f16 (2^-11) or,
     for fp32, two f16 parts (2^-22), exp2 is off by 2^-22 and its argument's rounding by 2^-23 |x - m|,
-    the sums by the number of their terms in a lane: 64 half steps + 20 for each merge."""
+    the sums by the number of their terms in a lane: 64 half steps + 20 for each merge.  The weighted values'
+    sums round 4 times a block and once for the offset, by up to a whole step of |value| + offset: 24 half steps."""
     B, Tq, H, d = q.shape
     Hkv = cache.Hkv
     G = H // Hkv
@@ -143,6 +156,7 @@ def attend(cache, q, n, *, g=None, bias=None, n_q=None, scale=None):
         written[b, :nq] = True
         for h in range(Hkv):
             k, v = rows_of(cache, "k", b, h, nb), rows_of(cache, "v", b, h, nb)
+            ka, va = k.abs() + offsets_of(cache, "k", b, h, nb), v.abs() + offsets_of(cache, "v", b, h, nb)
             bs = d64(bias[b, h, :nb]) if bias is not None else torch.zeros(nb, dtype=torch.float64)
             for i in range(nq):
                 see = max(0, nb - nq + i + 1)
@@ -150,9 +164,10 @@ def attend(cache, q, n, *, g=None, bias=None, n_q=None, scale=None):
                 if not keep.any():
                     continue
                 kk, vv, bb = k[keep], v[keep], bs[keep]
+                ka_, va_ = ka[keep], va[keep]
                 x0 = scale * d64(q[b, i, h * G:(h + 1) * G]) @ kk.T
                 x = x0 + bb
-                mag = abs(scale) * d64(q[b, i, h * G:(h + 1) * G]).abs() @ kk.abs().T
+                mag = abs(scale) * d64(q[b, i, h * G:(h + 1) * G]).abs() @ ka_.T
                 ex = (d + 8) * U32 * mag + (2.0 ** -21 * mag if f32 else 0) + 4 * U32 * (bb.abs() + x.abs())
                 m = x.max(-1, keepdim=True).values
                 p = torch.exp(x - m)
@@ -163,7 +178,7 @@ def attend(cache, q, n, *, g=None, bias=None, n_q=None, scale=None):
                 perr = each + (2.0 ** -21 if f32 else 2.0 ** -11)
                 hs = slice(h * G, (h + 1) * G)
                 o[b, i, hs] = p @ vv
-                ob[b, i, hs] = (p * perr) @ vv.abs() + zerr * (p @ vv.abs())
+                ob[b, i, hs] = (p * perr) @ vv.abs() + zerr * (p @ vv.abs()) + 24 * U32 * (p @ va_)
                 lse[b, hs, i] = (m + torch.log(z))[:, 0]
                 lb[b, hs, i] = zerr[:, 0] + 8 * U32 * (1 + m[:, 0].abs() + torch.log(z)[:, 0].abs())
     if g is not None:
