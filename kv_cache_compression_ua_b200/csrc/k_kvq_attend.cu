@@ -42,7 +42,6 @@ namespace {
 constexpr float kLog4e = 0.72134752044448170f;
 constexpr float kLn4 = 1.3862943611198906f;
 constexpr float kPShift = 14.f;             // probabilities are held as 2^14 p
-constexpr int kRingBytes = 16384;           // per warp
 constexpr int kUnitCost = 6;                // what starting and merging a unit costs, in blocks
 
 __device__ __forceinline__ float ex2(float x) {
@@ -150,17 +149,17 @@ template <typename T, int DH, int NT, bool E4M3> struct Att {
     static constexpr int PP = F32 ? 2 : 1;           // f16 parts of a probability
     static constexpr int TP = F32 ? 3 : 1;           // bf16 parts of an activation
     static constexpr int TPP = F32 ? 3 : 2;          // bf16 parts of a probability
-    static constexpr int NSTG = 128 / DH;            // blocks in a warp's ring
+    static constexpr int NSTG = 1;                   // blocks in a warp's ring
     static constexpr int KB = 64 * DH;               // bytes of a block's keys
     static constexpr int QS = DH + 4;                // row stride of the queries in shared memory
     static constexpr int NM = DH / 16;               // 16-element tiles of the output
     // One CTA an SM, of as many warps as its registers allow (168 or 255 a thread): few CTAs make few
     // parts to merge.
-    static constexpr int kWarps = NT == 1 ? 12 : 8, kThreads = 32 * kWarps;
+    static constexpr int kWarps = NT == 1 ? (DH == 64 ? 16 : 12) : 8, kThreads = 32 * kWarps;
     static constexpr int kBufs = kWarps / 4;         // buffers the warps' O are added up in
     static constexpr int kMinItems = kWarps + kUnitCost;    // fewest items (blocks and unit costs) of a run
     struct Smem {
-        alignas(128) unsigned char ring[kWarps][kRingBytes];
+        alignas(128) unsigned char ring[kWarps][NSTG * 2 * KB];
         alignas(16) float bias[kWarps][NSTG][kKvqBlock];
         alignas(16) uint16_t q16[QP][R][QS];         // f16, scaled by a power of two a row
         alignas(16) uint16_t qb[TP][R][QS];          // bf16 parts (for the unfinished block)
@@ -369,9 +368,20 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
     long long unit, hrow, rows[A::NSTG + 1];         // code rows of the steps in flight and of the one after
     const float* bias0;
     float ks, vs;
+    // This lane's places of a block (see k_place, v_place): where its first pieces are copied to, and where
+    // it reads from first; further ones lie at constant distances.
+    uint32_t ring_s;
+    int k_to, v_to, k_from, v_from;
 
     __device__ __forceinline__ Walk(const KvqAttendParams& p_, typename A::Smem& sm_)
-        : p(p_), sm(sm_), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), r(lane >> 2), c(lane & 3) {}
+        : p(p_), sm(sm_), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), r(lane >> 2), c(lane & 3) {
+        constexpr int PER = DH / 16;                     // 16-byte pieces of a token
+        ring_s = tc::smem_u32(sm.ring[warp]);
+        k_to = k_place<DH>(lane / PER, lane % PER);
+        v_to = v_place<DH>(lane / PER, lane % PER);
+        k_from = k_place<DH>(tok_of(r), c);
+        v_from = v_place<DH>(c, r >> 1) + 8 * (r & 1);
+    }
 
     __device__ __forceinline__ long long row_of(int i) const {
         if (i >= full) return i < steps ? kTail : kNone;
@@ -380,14 +390,12 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
     }
     // step i's keys (and bias) / values into place stg
     __device__ __forceinline__ void load_k(long long row, int i, int stg) {
-        const uint32_t dst = tc::smem_u32(sm.ring[warp]) + stg * 2 * A::KB;
+        const uint32_t dst = ring_s + stg * 2 * A::KB;
         if (row >= 0) {
-            const uint8_t* src = p.c.k + row * A::KB;
+            const uint8_t* src = p.c.k + row * A::KB + lane * 16;
 #pragma unroll
-            for (int j = 0; j < A::KB / 512; ++j) {
-                const int e = j * 32 + lane, tok = e / (DH / 16), ch = e % (DH / 16);
-                cp_async16(dst + k_place<DH>(tok, ch), src + e * 16);
-            }
+            for (int j = 0; j < A::KB / 512; ++j)        // (at 128 bytes a token, tokens 4 .. 7 of 8 are swapped by 64)
+                cp_async16(dst + (DH == 128 && (j & 1) ? k_to ^ 64 : k_to) + j * 512, src + j * 512);
             if (bias0 && lane < 16)
                 cp_async16(tc::smem_u32(&sm.bias[warp][stg][4 * lane]), bias0 + (first + i * kWarps) * kKvqBlock + 4 * lane);
         } else if (row == kTail) {
@@ -397,14 +405,11 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
         tc::cp_async_commit();
     }
     __device__ __forceinline__ void load_v(long long row, int stg) {
-        const uint32_t dst = tc::smem_u32(sm.ring[warp]) + (stg * 2 + 1) * A::KB;
+        const uint32_t dst = ring_s + (stg * 2 + 1) * A::KB;
         if (row >= 0) {
-            const uint8_t* src = p.c.v + row * A::KB;
+            const uint8_t* src = p.c.v + row * A::KB + lane * 16;
 #pragma unroll
-            for (int j = 0; j < A::KB / 512; ++j) {
-                const int e = j * 32 + lane, tok = e / (DH / 16), ch = e % (DH / 16);
-                cp_async16(dst + v_place<DH>(tok, ch), src + e * 16);
-            }
+            for (int j = 0; j < A::KB / 512; ++j) cp_async16(dst + v_to + j * 512, src + j * 512);
         } else if (row == kTail) {
             load_tail(dst, p.c.vr);
         }
@@ -505,9 +510,9 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
                         q[j][nt][s] = *reinterpret_cast<const uint2*>(&sm.q16[j][8 * nt + r][64 * hf + 16 * c + 4 * s]);
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                const int tok = 16 * mt + tok_of(r);
-                const uint4 u0 = *reinterpret_cast<const uint4*>(kb + k_place<DH>(tok, 4 * hf + c));
-                const uint4 u1 = *reinterpret_cast<const uint4*>(kb + k_place<DH>(tok + 8, 4 * hf + c));
+                const unsigned char* at = kb + (k_from ^ (hf << 6)) + 16 * mt * DH;
+                const uint4 u0 = *reinterpret_cast<const uint4*>(at);
+                const uint4 u1 = *reinterpret_cast<const uint4*>(at + 8 * DH);
                 const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
@@ -652,8 +657,7 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
                 uint2 w[4];                              // tokens 4k + c, elements 64 pass + 8r ..
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    w[k] = *reinterpret_cast<const uint2*>(vb + v_place<DH>(16 * kt + 4 * k + c, 4 * pass + (r >> 1)) +
-                                                           8 * (r & 1));
+                    w[k] = *reinterpret_cast<const uint2*>(vb + (v_from ^ (pass << 6)) + (16 * kt + 4 * k) * DH);
 #pragma unroll
                 for (int hw = 0; hw < 2; ++hw) {
                     const uint32_t t0 = hw ? w[0].y : w[0].x, t1 = hw ? w[1].y : w[1].x;
