@@ -95,11 +95,12 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
     constexpr int CH = DH / 16, HALF = DH / 2, NTH = 4 * DH, NW = NTH / 32, TOK = norm_tokens<DH, NTH>();
     constexpr int NV = KvQueue<T>::NV, DEPTH = KvQueue<T>::DEPTH;
     extern __shared__ __align__(16) unsigned char s_queue[];
-    __shared__ float s_cos[TOK * HALF], s_sin[TOK * HALF];
+    __shared__ __align__(16) float s_cos[TOK * HALF], s_sin[TOK * HALF];
     __shared__ double s_f[HALF];
     __shared__ uint32_t s_max[2][2][NW];
     __shared__ int s_last;
     grid_dep_wait();
+    grid_dep_release();
     const int tid = threadIdx.x, T_ = p.n.T, Hkv = p.c.Hkv;
     const int groups = Hkv / p.hpc, kv_ctas = p.c.B * groups * p.nb;
     // Every CTA arrives once it has read the slot counts; the last to arrive sets them, at its end.
@@ -115,13 +116,13 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
         const int i = blockIdx.x - kv_ctas, n0 = i / p.q_split * TOK;
         QkNormParams q = p.n;
         q.k = nullptr;
-        NormTile<T, DH, NTH>::run(q, n0, i % p.q_split, p.q_split, s_queue, [&](float* cs, float* sn) {
+        NormTile<T, DH, NTH>::run(q, n0, i % p.q_split, p.q_split, s_queue, [&](F2* cs, F2* sn) {
             auto posf = [&](int n) {
                 if (p.n.pos) return p.n.pos[n];
                 const int b = n / T_;
                 return (p.start ? p.start[b] : p.c.n_kept[b]) + n - b * T_;
             };
-            if (p.n.rope) tile_angles<DH, NTH>(s_cos, s_sin, n0, (int)p.n.N, p.n.rf, s_f, posf, cs, sn);
+            if (p.n.rope) tile_angles<T, DH, NTH>(s_cos, s_sin, n0, (int)p.n.N, p.n.rf, s_f, posf, cs, sn);
             arrive();                                    // (behind the angles' barrier)
         });
     } else {
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
         const int row = tid / CH, c = tid % CH;
         const SeqState s = seq_state(p, b);
         if (s.refused && j == 0 && gi == 0 && tid == 0) raise_status(s.refused);
-        if (tid < HALF) s_f[tid] = p.n.rf.f[tid];
+        if (tid < HALF) s_f[tid] = p.n.rf.f[tid] * 0.15915494309189535;      // 1 / (2 pi)
         __syncthreads();
         arrive();
         const int end = s.start + s.n_new, j0 = s.start / kKvqBlock, jl = end / kKvqBlock;   // jl: unfinished block
@@ -166,15 +167,16 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
                 const int hstep = old ? kKvqRing * DH : DH;
                 auto fetch = [&](int hh, int stage) {
                     if (hh < p.hpc) {
-                        const bool ok = is_new || old;
-                        const T* k = ok ? ksrc + hh * hstep : ksrc;
-                        const T* v = ok ? vsrc + hh * hstep : vsrc;
+                        if (is_new || old) {
+                            const T* k = ksrc + hh * hstep;
+                            const T* v = vsrc + hh * hstep;
 #pragma unroll
-                        for (int i = 0; i < NV; ++i) {
-                            queue.put(stage, i, k + i * Vec16<T>::N, ok);
-                            queue.put(stage, NV + i, k + HALF + i * Vec16<T>::N, ok);
-                            queue.put(stage, 2 * NV + i, v + i * Vec16<T>::N, ok);
-                            queue.put(stage, 3 * NV + i, v + HALF + i * Vec16<T>::N, ok);
+                            for (int i = 0; i < NV; ++i) {
+                                queue.put(stage, i, k + i * Vec16<T>::N);
+                                queue.put(stage, NV + i, k + HALF + i * Vec16<T>::N);
+                                queue.put(stage, 2 * NV + i, v + i * Vec16<T>::N);
+                                queue.put(stage, 3 * NV + i, v + HALF + i * Vec16<T>::N);
+                            }
                         }
                     }
                     queue.commit();
@@ -182,11 +184,11 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
 #pragma unroll
                 for (int i = 0; i < DEPTH - 1; ++i) fetch(i, i);
                 const long long crow = full ? kvq_row(p.c, b, blk) : -1;
-                float cs[8], sn[8];
+                F2 cs[4], sn[4], ns[4];
                 if (p.n.rope && is_new) {
                     const int pos = p.n.pos ? p.n.pos[n] : slot;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) rope_cs_pi(pos, s_f[8 * c + e], cs + e, sn + e);
+                    lane_angles<T>(pos, s_f, c, cs, sn);
+                    negate(sn, ns);
                 }
                 int stage = 0;
 #pragma unroll 1
@@ -200,20 +202,16 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
                         kb.u[i] = queue.get(stage, NV + i);
                     }
                     if (p.n.wk != nullptr || p.n.rope) {
-                        float x0[8], x1[8];
+                        F2 x0[4], x1[4];
                         ka.get(x0);
                         kb.get(x1);
                         if (p.n.wk != nullptr) {
-                            float w0[8], w1[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                w0[e] = __ldg(p.n.wk + 8 * c + e);
-                                w1[e] = __ldg(p.n.wk + HALF + 8 * c + e);
-                            }
+                            F2 w0[4], w1[4];
+                            load_gains<DH>(p.n.wk, c, w0, w1);
                             norm_row<DH>(x0, x1, w0, w1, p.n.eps);
                         }
                         if (is_new) {                    // rounded to the activation type: codes are formed
-                            if (p.n.rope) rotate_row(x0, x1, cs, sn);       // from what the ring would hold
+                            if (p.n.rope) rotate_row(x0, x1, cs, sn, ns);       // from what the ring would hold
                             ka.put(x0);
                             kb.put(x1);
                         }

@@ -80,6 +80,11 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
 // Four codes of a word -> two f16x2, exactly.  e4m3: codes 0, 1 and 2, 3.  int8: codes 0, 2 and 1, 3, each
 // as (code + 128) 2^-24: the byte with its sign bit flipped is the mantissa of a subnormal f16, so no
 // arithmetic is needed; the 128 are taken off by what the products' sums start from.
+__device__ __forceinline__ uint32_t and_xor(uint32_t w) {       // one instruction, the masks in registers
+    uint32_t y, keep = 0x00ff00ffu, flip = 0x00800080u;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(y) : "r"(w), "r"(keep), "r"(flip));
+    return y;
+}
 template <bool E4M3> __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
     if constexpr (E4M3) {
         asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
@@ -87,8 +92,8 @@ template <bool E4M3> __device__ __forceinline__ void codes_f16(uint32_t w, uint3
             : "=r"(lo), "=r"(hi)
             : "r"(w));
     } else {
-        lo = (w & 0x00ff00ffu) ^ 0x00800080u;
-        hi = ((w >> 8) & 0x00ff00ffu) ^ 0x00800080u;
+        lo = and_xor(w);
+        hi = and_xor(w >> 8);
     }
 }
 // Bytes of two tokens' words so that codes_f16 pairs the tokens: elements 0, 1 (k = 0) or 2, 3 (k = 1)

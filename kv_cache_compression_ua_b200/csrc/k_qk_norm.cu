@@ -12,25 +12,29 @@ namespace ua {
 
 constexpr int kNth = 256;               // threads of a CTA
 
-// grid (token tiles, head splits)
+// grid (token tiles, head splits).  p.beside: it runs beside the append of the same call, whose results
+// it does not need: that kernel releases it once everything before the call is done.
 template <typename T, int DH>
 __global__ void __launch_bounds__(kNth, 3) k_qk_norm_fwd(QkNormParams p) {
     constexpr int HALF = DH / 2, TOK = norm_tokens<DH, kNth>();
     extern __shared__ __align__(16) unsigned char s_queue[];
-    __shared__ float s_cos[TOK * HALF], s_sin[TOK * HALF];
+    __shared__ __align__(16) float s_cos[TOK * HALF], s_sin[TOK * HALF];
     __shared__ double s_f[HALF];
-    grid_dep_wait();
+    if (!p.beside) grid_dep_wait();
     const int n0 = blockIdx.x * TOK;
-    NormTile<T, DH, kNth>::run(p, n0, blockIdx.y, gridDim.y, s_queue, [&](float* cs, float* sn) {
-        if (p.rope)
-            tile_angles<DH, kNth>(s_cos, s_sin, n0, (int)p.N, p.rf, s_f,
-                                  [&](int n) { return p.pos ? p.pos[n] : (int)((unsigned)n % (unsigned)p.T); }, cs, sn);
+    NormTile<T, DH, kNth>::run(p, n0, blockIdx.y, gridDim.y, s_queue, [&](F2* cs, F2* sn) {
+        auto posf = [&](int n) {
+            if (p.pos) return p.pos[n];
+            const int b = (unsigned)n / (unsigned)p.T;
+            return n - b * p.T + (p.start ? p.start[b] : 0);
+        };
+        if (p.rope) tile_angles<T, DH, kNth>(s_cos, s_sin, n0, (int)p.N, p.rf, s_f, posf, cs, sn);
     });
+    if (p.beside) grid_dep_wait();                      // whoever waits for this kernel waits for that one
 }
 
 // Backward.  The first ctas_q CTAs take the queries, the others the keys (in proportion to their
-// heads).  A persistent CTA walks token tiles; the loads of the next head quads, the next tile's
-// among them, are always on their way (a thread's own queue in shared memory).  It keeps the gain
+// heads), each an equal run of (token tile, four heads) items; the loads of the next items are always on their way (a thread's own queue in shared memory).  It keeps the gain
 // gradient of its lanes' elements in registers (fp32), sums it over its rows in shared memory at the
 // end and writes one partial row; k_qk_norm_dw adds the CTAs' rows in a fixed order.
 template <typename T> struct BwdQueue {
@@ -38,144 +42,163 @@ template <typename T> struct BwdQueue {
     using Queue = LaneQueue<kNth, 4 * NV, DEPTH>;
 };
 
-template <typename T, int DH>
-__global__ void __launch_bounds__(kNth, 2) k_qk_norm_bwd(QkNormParams p, int ctas_q) {
+template <typename T, int DH, bool ROPE, bool NORM>
+__device__ __forceinline__ void bwd_run(const QkNormParams& p, bool is_q, int cta, int ctas, unsigned char* s_queue,
+                                        const double* s_f) {
     constexpr int CH = DH / 16, HALF = DH / 2, TOK = norm_tokens<DH, kNth>(), ROWS = kNth / CH;
     constexpr int NV = BwdQueue<T>::NV, DEPTH = BwdQueue<T>::DEPTH;
-    extern __shared__ __align__(16) unsigned char s_queue[];
-    __shared__ float s_cos[TOK * HALF], s_sin[TOK * HALF];
-    __shared__ double s_f[HALF];
-    static_assert(BwdQueue<T>::Queue::kBytes >= ROWS * DH * 4, "the rows' sums fit the queue");
-    grid_dep_wait();
     const int tid = threadIdx.x, c = tid % CH, hp = (tid / CH) % kNormHeads, row = tid / CH, N = (int)p.N;
-    const bool is_q = (int)blockIdx.x < ctas_q;
-    const int first = is_q ? blockIdx.x : blockIdx.x - ctas_q, step = is_q ? ctas_q : gridDim.x - ctas_q;
-    const T* x = static_cast<const T*>(is_q ? p.q : p.k);
     const T* dy = static_cast<const T*>(is_q ? p.dq_out : p.dk_out);
-    T* dx = static_cast<T*>(is_q ? p.dq : p.dk);
-    const float* w = is_q ? p.wq : p.wk;
     const int nh = is_q ? p.H : p.Hkv, quads = (nh + kNormHeads - 1) / kNormHeads;
     const long long ld = is_q ? p.q_ld : p.k_ld;
+    // an equal run of (token tile, head quad) items
     const int tiles = (N + TOK - 1) / TOK;
+    const int lo = (int)((long long)tiles * quads * cta / ctas);
+    const int count = (int)((long long)tiles * quads * (cta + 1) / ctas) - lo;
     typename BwdQueue<T>::Queue queue(s_queue);
-    int ft = first, fi = 0, fstage = 0;              // the next (tile, quad) to fetch
+    // the next item to fetch: its place in dy (and dx) and in x
+    int left = count, fi = lo % quads, fn = lo / quads * TOK + row / kNormHeads, fstage = 0;
+    const T* fg = dy + ((long long)fn * nh + fi * kNormHeads + hp) * DH + 8 * c;
+    const T* fx = static_cast<const T*>(is_q ? p.q : p.k) + fn * ld + (fi * kNormHeads + hp) * DH + 8 * c;
+    const long long g_jump = ((long long)TOK * nh - (quads - 1) * kNormHeads) * DH;   // from a tile's last quad to the
+    const long long x_jump = TOK * ld - (long long)(quads - 1) * kNormHeads * DH;     // next tile's first
     auto fetch = [&]() {
-        if (ft < tiles) {
-            const int n = ft * TOK + row / kNormHeads, h = fi * kNormHeads + hp;
-            const bool ok = n < N && h < nh;
-            const T* g = ok ? dy + ((long long)n * nh + h) * DH + 8 * c : dy;
-            const T* s = ok ? x + n * ld + h * DH + 8 * c : x;
+        if (left > 0) {
+            --left;
+            if (fn < N && fi * kNormHeads + hp < nh) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                queue.put(fstage, v, g + v * Vec16<T>::N, ok);
-                queue.put(fstage, NV + v, g + HALF + v * Vec16<T>::N, ok);
-                if (w != nullptr) {
-                    queue.put(fstage, 2 * NV + v, s + v * Vec16<T>::N, ok);
-                    queue.put(fstage, 3 * NV + v, s + HALF + v * Vec16<T>::N, ok);
+                for (int v = 0; v < NV; ++v) {
+                    queue.put(fstage, v, fg + v * Vec16<T>::N);
+                    queue.put(fstage, NV + v, fg + HALF + v * Vec16<T>::N);
+                    if (NORM) {
+                        queue.put(fstage, 2 * NV + v, fx + v * Vec16<T>::N);
+                        queue.put(fstage, 3 * NV + v, fx + HALF + v * Vec16<T>::N);
+                    }
                 }
             }
             if (++fi == quads) {
                 fi = 0;
-                ft += step;
+                fn += TOK;
+                fg += g_jump;
+                fx += x_jump;
+            } else {
+                fg += kNormHeads * DH;
+                fx += kNormHeads * DH;
             }
         }
         queue.commit();
-        fstage = (fstage + 1) % DEPTH;
+        fstage = fstage + 1 == DEPTH ? 0 : fstage + 1;
     };
+    int i = fi, n = fn, stage = 0;
+    T* out = static_cast<T*>(is_q ? p.dq : p.dk) + (fg - dy);
 #pragma unroll
-    for (int i = 0; i < DEPTH - 1; ++i) fetch();
-    float w0[8], w1[8], dw[16];
+    for (int j = 0; j < DEPTH - 1; ++j) fetch();
+    F2 w0[4], w1[4], dw[8], cs[4], sn[4], ns[4];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) dw[e] = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        w0[e] = w ? __ldg(w + 8 * c + e) : 1.f;
-        w1[e] = w ? __ldg(w + HALF + 8 * c + e) : 1.f;
-    }
-    int stage = 0;
-    for (int tile = first; tile < tiles; tile += step) {
-        const int n0 = tile * TOK, n = n0 + row / kNormHeads;
-        float cs[8], sn[8];
-        if (p.rope) {
-            __syncthreads();                            // the last tile's angles have been read
-            tile_angles<DH, kNth>(s_cos, s_sin, n0, N, p.rf, s_f,
-                                  [&](int m) { return p.pos ? p.pos[m] : (int)((unsigned)m % (unsigned)p.T); }, cs, sn);
+    for (int j = 0; j < 8; ++j) dw[j] = f2(0.f, 0.f);
+    if (NORM) load_gains<DH>(is_q ? p.wq : p.wk, c, w0, w1);
+    const float eps = p.eps;
+    auto pos_of = [&](int m) { return m >= N ? 0 : p.pos ? __ldg(p.pos + m) : (int)((unsigned)m % (unsigned)p.T); };
+    int pos = ROPE ? pos_of(n) : 0;
+    bool new_tile = true;
+#pragma unroll 1
+    for (int item = 0; item < count; ++item) {
+        if (ROPE && new_tile) {                         // (its position was fetched with the tile before)
+            lane_angles<T>(pos, s_f, c, cs, sn);
+            negate(sn, ns);
+            pos = pos_of(n + TOK);
         }
-        for (int i = 0; i < quads; ++i) {
-            const int h = i * kNormHeads + hp;
-            const bool ok = n < N && h < nh;
-            fetch();
-            queue.template wait<DEPTH - 1>();
-            Raw8<T> ga, gb;
-            float g0[8], g1[8];
+        const bool ok = n < N && i * kNormHeads + hp < nh;
+        fetch();
+        queue.template wait<DEPTH - 1>();
+        Raw8<T> ga, gb;
+        F2 g0[4], g1[4];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            ga.u[v] = queue.get(stage, v);
+            gb.u[v] = queue.get(stage, NV + v);
+        }
+        ga.get(g0);
+        gb.get(g1);
+        if (ROPE) rotate_row(g0, g1, cs, ns, sn);       // R(-pos) dy
+        if (NORM) {
+            Raw8<T> xa, xb;
+            F2 x0[4], x1[4], n0[4], n1[4];              // n: g (.) w
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                ga.u[v] = queue.get(stage, v);
-                gb.u[v] = queue.get(stage, NV + v);
+                xa.u[v] = queue.get(stage, 2 * NV + v);
+                xb.u[v] = queue.get(stage, 3 * NV + v);
             }
-            ga.get(g0);
-            gb.get(g1);
-            if (p.rope) {                               // R(-pos) dy
+            xa.get(x0);
+            xb.get(x1);
+            F2 ss = f2(0.f, 0.f), dot = ss;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float u = g0[e], v = g1[e];
-                    g0[e] = u * cs[e] + v * sn[e];
-                    g1[e] = v * cs[e] - u * sn[e];
+            for (int j = 0; j < 4; ++j) {
+                n0[j] = mul2(g0[j], w0[j]);
+                n1[j] = mul2(g1[j], w1[j]);
+                ss = fma2(x0[j], x0[j], fma2(x1[j], x1[j], ss));
+                dot = fma2(n0[j], x0[j], fma2(n1[j], x1[j], dot));
+            }
+            const float r = rsqrtf(row_sum<CH>(hsum(ss)) * (1.f / DH) + eps);
+            const float rm = r * row_sum<CH>(hsum(dot)) * r * (1.f / DH);    // r * mean(n (.) xh)
+            if (ok) {                                   // (a row past the end holds anything)
+                const F2 r2 = f2(r, r), m2 = f2(-rm, -rm);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const F2 h0 = mul2(x0[j], r2), h1 = mul2(x1[j], r2);
+                    dw[j] = fma2(g0[j], h0, dw[j]);
+                    dw[4 + j] = fma2(g1[j], h1, dw[4 + j]);
+                    g0[j] = fma2(h0, m2, mul2(n0[j], r2));
+                    g1[j] = fma2(h1, m2, mul2(n1[j], r2));
                 }
             }
-            if (w != nullptr) {
-                Raw8<T> xa, xb;
-                float x0[8], x1[8], ss = 0.f, dot = 0.f;
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    xa.u[v] = queue.get(stage, 2 * NV + v);
-                    xb.u[v] = queue.get(stage, 3 * NV + v);
-                }
-                xa.get(x0);
-                xb.get(x1);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    ss = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], ss));
-                    dot = fmaf(g0[e] * w0[e], x0[e], fmaf(g1[e] * w1[e], x1[e], dot));
-                }
-                const float r = rsqrtf(row_sum<CH>(ss) * (1.f / DH) + p.eps);
-                const float rm = r * row_sum<CH>(dot) * r * (1.f / DH);      // r * mean(n' (.) xh)
-                if (ok) {                               // (a row past the end would add 0 * rsqrt(eps))
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float h0 = x0[e] * r, h1 = x1[e] * r;
-                        dw[e] = fmaf(g0[e], h0, dw[e]);
-                        dw[8 + e] = fmaf(g1[e], h1, dw[8 + e]);
-                        g0[e] = fmaf(r, g0[e] * w0[e], -h0 * rm);
-                        g1[e] = fmaf(r, g1[e] * w1[e], -h1 * rm);
-                    }
-                }
-            }
-            stage = (stage + 1) % DEPTH;
-            if (ok) {
-                T* d = dx + ((long long)n * nh + h) * DH + 8 * c;
-                ga.put(g0);
-                gb.put(g1);
-                ga.st(d);
-                gb.st(d + HALF);
-            }
+        }
+        stage = stage + 1 == DEPTH ? 0 : stage + 1;
+        if (ok) {
+            ga.put(g0);
+            gb.put(g1);
+            ga.st(out);
+            gb.st(out + HALF);
+        }
+        new_tile = ++i == quads;
+        if (new_tile) {
+            i = 0;
+            n += TOK;
+            out += g_jump;
+        } else {
+            out += kNormHeads * DH;
         }
     }
     queue.template wait<0>();
-    if (w == nullptr) return;
+    if (!NORM) return;
     __syncthreads();                                    // the queue becomes the rows' sums [row][element]
     float* s_sum = reinterpret_cast<float*>(s_queue);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        s_sum[row * DH + 8 * c + e] = dw[e];
-        s_sum[row * DH + HALF + 8 * c + e] = dw[8 + e];
-    }
+    float* mine = s_sum + row * DH + 8 * c;
+    unpairs(dw, mine);
+    unpairs(dw + 4, mine + HALF);
     __syncthreads();
     if (tid < DH) {
         float s = 0.f;
         for (int r = 0; r < ROWS; ++r) s += s_sum[r * DH + tid];
         p.part[(size_t)blockIdx.x * DH + tid] = s;
     }
+}
+
+template <typename T, int DH, bool ROPE>
+__global__ void __launch_bounds__(kNth, 2) k_qk_norm_bwd(const __grid_constant__ QkNormParams p, int ctas_q) {
+    extern __shared__ __align__(16) unsigned char s_queue[];
+    __shared__ double s_f[DH / 2];
+    static_assert(BwdQueue<T>::Queue::kBytes >= kNth / (DH / 16) * DH * 4, "the rows' sums fit the queue");
+    grid_dep_wait();
+    grid_dep_release();                                 // (k_qk_norm_dw may be made ready)
+    if (ROPE) {
+        if (threadIdx.x < DH / 2) s_f[threadIdx.x] = p.rf.f[threadIdx.x] * 0.15915494309189535;  // 1 / (2 pi)
+        __syncthreads();
+    }
+    const bool is_q = (int)blockIdx.x < ctas_q;
+    const int cta = is_q ? blockIdx.x : blockIdx.x - ctas_q, ctas = is_q ? ctas_q : gridDim.x - ctas_q;
+    if ((is_q ? p.wq : p.wk) != nullptr) bwd_run<T, DH, ROPE, true>(p, is_q, cta, ctas, s_queue, s_f);
+    else bwd_run<T, DH, ROPE, false>(p, is_q, cta, ctas, s_queue, s_f);
 }
 
 // Sum of the CTAs' partial gain gradients: grid (d/32, 2), block (32, 32); rows [0, ctas_q) are the
@@ -223,14 +246,16 @@ template <typename T, int DH> cudaError_t bwd(const QkNormParams& p, cudaStream_
     const int nq = p.q ? p.H : 0, nk = p.k ? p.Hkv : 0;
     auto most = [&](int heads) {
         const long long n = heads ? (kQkNormBwdCtas * (long long)heads + (nq + nk) / 2) / (nq + nk) : 0;
-        return (int)(heads == 0 ? 0 : n < 1 ? 1 : n < tiles ? n : tiles);
+        const long long items = tiles * ((heads + kNormHeads - 1) / kNormHeads);
+        return (int)(heads == 0 ? 0 : n < 1 ? 1 : n < items ? n : items);
     };
     const int ctas_q = most(nq), ctas = ctas_q + most(nk);
-    cudaError_t e = cudaFuncSetAttribute(k_qk_norm_bwd<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    auto kern = p.rope ? k_qk_norm_bwd<T, DH, true> : k_qk_norm_bwd<T, DH, false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     {
         UA_PROFILE("k_qk_norm_bwd", s);
-        e = launch_dependent(k_qk_norm_bwd<T, DH>, dim3(ctas), dim3(kNth), smem, s, p, ctas_q);
+        e = launch_dependent(kern, dim3(ctas), dim3(kNth), smem, s, p, ctas_q);
         if (e != cudaSuccess) return e;
     }
     float* dwq = p.q && p.wq ? p.dwq : nullptr;

@@ -7,6 +7,50 @@
 
 namespace ua {
 
+// Two fp32 operations an instruction (sm_100a's packed arithmetic): the norm kernels would otherwise be
+// bound by instruction issue before memory.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void un2(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 neg2(F2 a) { return F2{a.v ^ 0x8000000080000000ull}; }
+__device__ __forceinline__ float hsum(F2 a) {
+    float x, y;
+    un2(a, x, y);
+    return x + y;
+}
+// 8 floats as 4 pairs
+__device__ __forceinline__ void pairs16(const float* x, F2* p) {   // x 16-byte aligned
+    const float4 a = reinterpret_cast<const float4*>(x)[0], b = reinterpret_cast<const float4*>(x)[1];
+    p[0] = f2(a.x, a.y);
+    p[1] = f2(a.z, a.w);
+    p[2] = f2(b.x, b.y);
+    p[3] = f2(b.z, b.w);
+}
+__device__ __forceinline__ void pairs(const float* x, F2* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = f2(x[2 * i], x[2 * i + 1]);
+}
+__device__ __forceinline__ void unpairs(const F2* p, float* x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) un2(p[i], x[2 * i], x[2 * i + 1]);
+}
+
 // 8 activations as loaded: one 16-byte vector (bf16) or two (f32).
 template <typename T> struct Raw8 {
     static constexpr int NV = sizeof(T) / 2;
@@ -22,6 +66,16 @@ template <typename T> struct Raw8 {
     __device__ __forceinline__ void get(float* x) const {
 #pragma unroll
         for (int i = 0; i < NV; ++i) Vec16<T>::unpack(u[i], x + i * Vec16<T>::N);
+    }
+    __device__ __forceinline__ void get(F2* p) const {
+        float x[8];
+        get(x);
+        pairs(x, p);
+    }
+    __device__ __forceinline__ void put(const F2* p) {
+        float x[8];
+        unpairs(p, x);
+        put(x);
     }
     // rounds to the activation type (once)
     __device__ __forceinline__ void put(const float* x) {
@@ -61,11 +115,18 @@ template <typename T> struct Raw8 {
     }
 };
 
-// cos / sin of pos * f: the angle in turns is formed in double precision and its nearest integer
-// removed exactly, so far positions keep the accuracy of the fp32 sine of the remainder.
-__device__ __forceinline__ void rope_cs_pi(int pos, double f, float* c, float* s) {
-    const double a = (double)pos * (f * 0.15915494309189535);      // 1 / (2 pi)
-    sincospif(2.f * (float)(a - rint(a)), s, c);
+// cos / sin of pos * f, given gt = f / (2 pi): the angle in turns is formed in double precision and its
+// nearest integer removed exactly, so far positions keep the accuracy of the sine of the remainder.
+// fp32 results take sincospi (1 to 2 ulp); bf16 ones the fast unit, whose absolute error on
+// [-pi, pi], below 2^-20, is far under their half step of 2^-9 of the pair's size.
+template <typename T> __device__ __forceinline__ void rope_cs_turn(int pos, double gt, float* c, float* s) {
+    const double a = (double)pos * gt;
+    const float r = (float)(a - rint(a));
+    if constexpr (sizeof(T) == 4) {
+        sincospif(2.f * r, s, c);
+    } else {
+        __sincosf(6.28318530717958648f * r, s, c);
+    }
 }
 
 // Rows are spread over a CTA as CH = DH/16 consecutive lanes a head, each lane with elements
@@ -76,26 +137,33 @@ template <int CH> __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-template <int DH> __device__ __forceinline__ void norm_row(float* x0, float* x1, const float* w0, const float* w1,
-                                                           float eps) {
-    float ss = 0.f;
+template <int DH> __device__ __forceinline__ void norm_row(F2* x0, F2* x1, const F2* w0, const F2* w1, float eps) {
+    F2 ss = mul2(x0[0], x0[0]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], ss));
-    const float r = rsqrtf(row_sum<DH / 16>(ss) * (1.f / DH) + eps);
+    for (int i = 1; i < 4; ++i) ss = fma2(x0[i], x0[i], ss);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        x0[e] = x0[e] * r * w0[e];
-        x1[e] = x1[e] * r * w1[e];
+    for (int i = 0; i < 4; ++i) ss = fma2(x1[i], x1[i], ss);
+    const float r = rsqrtf(row_sum<DH / 16>(hsum(ss)) * (1.f / DH) + eps);
+    const F2 r2 = f2(r, r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x0[i] = mul2(mul2(x0[i], r2), w0[i]);
+        x1[i] = mul2(mul2(x1[i], r2), w1[i]);
     }
 }
 
-__device__ __forceinline__ void rotate_row(float* x0, float* x1, const float* cs, const float* sn) {
+// R(pos) x; with -sn for sn and sn for ns (the negated sines), R(-pos) x
+__device__ __forceinline__ void rotate_row(F2* x0, F2* x1, const F2* cs, const F2* sn, const F2* ns) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float a = x0[e], b = x1[e];
-        x0[e] = a * cs[e] - b * sn[e];
-        x1[e] = b * cs[e] + a * sn[e];
+    for (int i = 0; i < 4; ++i) {
+        const F2 a = x0[i], b = x1[i];
+        x0[i] = fma2(b, ns[i], mul2(a, cs[i]));
+        x1[i] = fma2(a, sn[i], mul2(b, cs[i]));
     }
+}
+__device__ __forceinline__ void negate(const F2* a, F2* b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = neg2(a[i]);
 }
 
 // Geometry of the norm kernels: NTH threads take NTH / CH rows at a time, as 4 heads of
@@ -111,9 +179,9 @@ template <int NTH, int PIECES, int DEPTH> struct LaneQueue {
     static constexpr int kBytes = NTH * PIECES * DEPTH * 16;
     uint4* base;                                     // this thread's first piece
     __device__ __forceinline__ LaneQueue(void* smem) : base(static_cast<uint4*>(smem) + threadIdx.x) {}
-    __device__ __forceinline__ void put(int stage, int piece, const void* src, bool ok) {
+    __device__ __forceinline__ void put(int stage, int piece, const void* src) {
         const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(base + (stage * PIECES + piece) * NTH));
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
     }
     __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
     template <int PENDING> __device__ __forceinline__ void wait() {
@@ -124,25 +192,41 @@ template <int NTH, int PIECES, int DEPTH> struct LaneQueue {
 
 // cos / sin of a tile's tokens into shared memory ([tokens][DH/2] each), then this thread's eight.
 // posf(n): position of flat token n.
-template <int DH, int NTH, typename F>
+template <typename T, int DH, int NTH, typename F>
 __device__ __forceinline__ void tile_angles(float* s_cos, float* s_sin, int n0, int N, const RopeFreq& rf,
-                                            double* s_f, F posf, float* cs, float* sn) {
+                                            double* s_f, F posf, F2* cs, F2* sn) {
     constexpr int HALF = DH / 2, TOK = norm_tokens<DH, NTH>();
     const int tid = threadIdx.x;
-    if (tid < HALF) s_f[tid] = rf.f[tid];
+    if (tid < HALF) s_f[tid] = rf.f[tid] * 0.15915494309189535;      // 1 / (2 pi)
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < TOK * HALF / NTH; ++i) {
         const int e = i * NTH + tid, tk = e / HALF, m = e % HALF;
         const int n = n0 + tk;
-        rope_cs_pi(n < N ? posf(n) : 0, s_f[m], s_cos + e, s_sin + e);
+        rope_cs_turn<T>(n < N ? posf(n) : 0, s_f[m], s_cos + e, s_sin + e);
     }
     __syncthreads();
     const int c = tid % (DH / 16), tk = tid / (DH / 16) / kNormHeads;
+    pairs16(s_cos + tk * HALF + 8 * c, cs);
+    pairs16(s_sin + tk * HALF + 8 * c, sn);
+}
+// A thread's own 8 angles at position pos; s_f: f / (2 pi) of the DH/2 pairs.
+template <typename T> __device__ __forceinline__ void lane_angles(int pos, const double* s_f, int c, F2* cs, F2* sn) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        cs[e] = s_cos[tk * HALF + 8 * c + e];
-        sn[e] = s_sin[tk * HALF + 8 * c + e];
+    for (int i = 0; i < 4; ++i) {
+        float ca, sa, cb, sb;
+        rope_cs_turn<T>(pos, s_f[8 * c + 2 * i], &ca, &sa);
+        rope_cs_turn<T>(pos, s_f[8 * c + 2 * i + 1], &cb, &sb);
+        cs[i] = f2(ca, cb);
+        sn[i] = f2(sa, sb);
+    }
+}
+// 8 gains of each half
+template <int DH> __device__ __forceinline__ void load_gains(const float* w, int c, F2* w0, F2* w1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w0[i] = f2(__ldg(w + 8 * c + 2 * i), __ldg(w + 8 * c + 2 * i + 1));
+        w1[i] = f2(__ldg(w + DH / 2 + 8 * c + 2 * i), __ldg(w + DH / 2 + 8 * c + 2 * i + 1));
     }
 }
 
@@ -165,30 +249,30 @@ template <typename T, int DH, int NTH> struct NormTile {
                 const int h = (is_q ? i : i - nq4) * kNormHeads + hp;
                 const bool ok = n < N && h < (is_q ? p.H : p.Hkv);
                 const T* x = is_q ? static_cast<const T*>(p.q) : static_cast<const T*>(p.k);
-                const T* s = ok ? x + (long long)n * (is_q ? p.q_ld : p.k_ld) + h * DH + 8 * c : x;
+                const T* s = x + (long long)n * (is_q ? p.q_ld : p.k_ld) + h * DH + 8 * c;
+                if (ok) {
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    queue.put(stage, v, s + v * Vec16<T>::N, ok);
-                    queue.put(stage, NV + v, s + HALF + v * Vec16<T>::N, ok);
+                    for (int v = 0; v < NV; ++v) {
+                        queue.put(stage, v, s + v * Vec16<T>::N);
+                        queue.put(stage, NV + v, s + HALF + v * Vec16<T>::N);
+                    }
                 }
             }
             queue.commit();
         };
 #pragma unroll
         for (int i = 0; i < DEPTH - 1; ++i) fetch(y + i * ny, i);
-        float cs[8], sn[8], w0[8], w1[8];
+        F2 cs[4], sn[4], w0[4], w1[4];
         angles(cs, sn);
+        F2 ns[4];
+        negate(sn, ns);
         const float* have = nullptr;                    // gain the registers hold
         int stage = 0;
         for (int i = y; i < all; i += ny) {
             const bool is_q = i < nq4;
             const float* w = is_q ? p.wq : p.wk;
             if (w != nullptr && w != have) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    w0[e] = __ldg(w + 8 * c + e);
-                    w1[e] = __ldg(w + HALF + 8 * c + e);
-                }
+                load_gains<DH>(w, c, w0, w1);
                 have = w;
             }
             fetch(i + (DEPTH - 1) * ny, (stage + DEPTH - 1) % DEPTH);
@@ -200,11 +284,11 @@ template <typename T, int DH, int NTH> struct NormTile {
                 b.u[v] = queue.get(stage, NV + v);
             }
             stage = (stage + 1) % DEPTH;
-            float x0[8], x1[8];
+            F2 x0[4], x1[4];
             a.get(x0);
             b.get(x1);
             if (w != nullptr) norm_row<DH>(x0, x1, w0, w1, p.eps);
-            if (p.rope) rotate_row(x0, x1, cs, sn);
+            if (p.rope) rotate_row(x0, x1, cs, sn, ns);
             const int h = (is_q ? i : i - nq4) * kNormHeads + hp;
             if (n < N && h < (is_q ? p.H : p.Hkv)) {
                 T* d = is_q ? static_cast<T*>(p.q_out) + ((long long)n * p.H + h) * DH + 8 * c

@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kVersion = 100;   // 0.1.0
 constexpr int kBq = 64;         // query tile height of the SIMT attention path
+constexpr int kAppendCtas = 111;        // CTAs an append should have (3/4 of the SMs) before heads share one
 constexpr int kMaxCapacity = 1 << 20;   // decode keeps a capacity/32-word bitmap in shared memory
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -1007,23 +1008,32 @@ ua_status ua_kvq_append(const ua_kvq* c, const ua_qk_shape* s, const void* q, co
     p.v_ld = s->v_ld ? s->v_ld : (long long)s->Hkv * s->d;
     p.n_new = n_new; p.start = start;
     p.nb = (int)(((long long)s->T + 2 * kKvqBlock - 2) / kKvqBlock);
-    // all KV heads in one CTA share a token's angles; fewer heads a CTA where the blocks alone do
-    // not fill the GPU
+    // all KV heads in one CTA share a token's angles; fewer heads a CTA where the blocks alone leave SMs idle
     p.hpc = s->Hkv;
-    while (p.hpc > 1 && (long long)s->B * p.nb * (s->Hkv / p.hpc) < 2 * 148) {
+    while (p.hpc > 1 && (long long)s->B * p.nb * (s->Hkv / p.hpc) < kAppendCtas) {
         int next = p.hpc - 1;
         while (s->Hkv % next) --next;
         p.hpc = next;
     }
-    if (q) {
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    // The queries of many tokens run in their own kernel beside the blocks' one (smaller CTAs, more of
+    // them an SM); those of a few steps in further CTAs of the same launch, as do queries whose positions
+    // are slot counts that this call changes.
+    const bool apart = q && p.n.N >= 148 * 16 && (pos || start || !p.n.rope);
+    if (q && !apart) {
         p.q_tiles = (int)((p.n.N + 15) / 16);
         const int quads = (s->H + 3) / 4;
         p.q_split = p.q_tiles >= 148 ? 1 : std::min(quads, std::max(1, 148 / p.q_tiles));
     }
     if ((long long)s->B * (s->Hkv / p.hpc) * p.nb + (long long)p.q_tiles * p.q_split > INT32_MAX)
         return UA_ERR_UNSUPPORTED;
-    return cuda_status(launch_kvq_append(p, s->d, s->dtype == UA_BF16, c->format == UA_KVQ_E4M3,
-                                         static_cast<cudaStream_t>(stream)));
+    st = cuda_status(launch_kvq_append(p, s->d, s->dtype == UA_BF16, c->format == UA_KVQ_E4M3, cs));
+    if (st != UA_OK || !apart) return st;
+    QkNormParams n = p.n;
+    n.k = nullptr;
+    n.start = start;
+    n.beside = 1;
+    return cuda_status(launch_qk_norm_fwd(n, s->d, s->dtype == UA_BF16, cs));
 }
 
 ua_status ua_kvq_attend_workspace_size(const ua_kvq* c, int H, int Tq, size_t* bytes) {

@@ -348,7 +348,9 @@ struct QkNormParams {
     const void* k;
     const float* wq;               // [d] or NULL: no norm
     const float* wk;
-    const int32_t* pos;            // [N] or NULL: t
+    const int32_t* pos;            // [N] or NULL: t, from start[b] on (forward; NULL: 0)
+    const int32_t* start;
+    int beside;                    // forward: runs beside the kernel before it (see k_qk_norm_fwd)
     void* q_out;
     void* k_out;
     // backward

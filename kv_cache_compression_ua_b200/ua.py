@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -593,20 +594,37 @@ def decode_step(cache: Cache, q, k, v, g, a_q, a_k, alpha, beta, pos_t: int, p: 
 
 
 # ------------------------------------------------------------------ softmax layers
+def _bad(name, t, shape, dtypes, dev):
+    """The first thing wrong with an output or side input that should be `shape`, one of dtypes, dense, on dev."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {list(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, the call runs on {dev}")
+    raise ValueError("libua takes contiguous tensors")
+
+
+def _dense(name, t, shape, dtypes, dev):
+    if t is not None and (t.shape != shape or t.dtype not in dtypes or t.device != dev or not t.is_contiguous()):
+        _bad(name, t, shape, dtypes, dev)
+
+
 def _heads(name, t, B, T, d, dtype, dev):
     """Checks an input [B, T, heads, d] whose tokens' heads are contiguous (a dense tensor, or a slice
-    of a fused projection's output) and returns (heads, elements between tokens)."""
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != T or t.shape[3] != d:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{B}, {T}, heads, {d}]")
+    of a fused projection's output) and returns (heads, elements between tokens; 0: dense)."""
+    s = t.shape
+    if len(s) != 4 or s[0] != B or s[1] != T or s[3] != d:
+        raise ValueError(f"{name}: shape {tuple(s)}, expected [{B}, {T}, heads, {d}]")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.device != dev:
         raise ValueError(f"{name}: on {t.device}, the call runs on {dev}")
     if not t.is_cuda:
         raise ValueError("libua takes CUDA tensors")
-    n = t.shape[2]
+    n = s[2]
     if t.is_contiguous():
-        return n, n * d
+        return n, 0
     sb, st, sh, se = t.stride()
     ld = st if T > 1 else (sb if B > 1 else n * d)
     if se != 1 or (n > 1 and sh != d) or (B > 1 and sb != T * ld) or ld < n * d:
@@ -614,18 +632,9 @@ def _heads(name, t, B, T, d, dtype, dev):
     return n, ld
 
 
-def _dense(name, t, shape, dtypes, dev):
-    """Checks an output or side input of exactly this shape, dense."""
-    if t is None:
-        return
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {list(shape)}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, the call runs on {dev}")
-    if not t.is_contiguous():
-        raise ValueError("libua takes contiguous tensors")
+def _like(x):
+    """A dense tensor like x (which may be a slice of a larger one)."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _addr(t):
@@ -636,26 +645,49 @@ def _raw_stream(stream, dev):
     return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
 
 
+def _launch(name, dev, fn, *args):
+    """Call the library with dev current (it launches on the current device)."""
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args)
+    if rc != 0:
+        raise UAError(name, rc)
+
+
+@functools.lru_cache(maxsize=256)
+def _qk_struct(*fields):
+    return ua_qk_shape(*fields)
+
+
 def _qk_shape(q, k, wq, wk, pos, eps, theta, v=None):
-    """(shape, device) of a norm / append call from its checked inputs (q or k may be None)."""
+    """(shape, device, activation dtype) of a norm / append call from its checked inputs (q or k may be
+    None)."""
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k: at least one of them is needed")
     if x.dim() != 4:
         raise ValueError(f"q or k: shape {tuple(x.shape)}, expected [B, T, heads, d]")
     B, T, _, d = x.shape
-    dev = x.device
-    H, q_ld = _heads("q", q, B, T, d, x.dtype, dev) if q is not None else (1, 0)
-    Hkv, k_ld = _heads("k", k, B, T, d, x.dtype, dev) if k is not None else (1, 0)
+    dev, dt = x.device, x.dtype
+    H, q_ld = _heads("q", q, B, T, d, dt, dev) if q is not None else (1, 0)
+    Hkv, k_ld = _heads("k", k, B, T, d, dt, dev) if k is not None else (1, 0)
     v_ld = 0
     if v is not None:
-        hv, v_ld = _heads("v", v, B, T, d, x.dtype, dev)
+        hv, v_ld = _heads("v", v, B, T, d, dt, dev)
         if hv != Hkv:
             raise ValueError(f"v: {hv} heads, expected {Hkv}")
-    _dense("wq", wq, (d,), F32, dev)
-    _dense("wk", wk, (d,), F32, dev)
-    _dense("pos", pos, (B, T), (torch.int32,), dev)
-    return ua_qk_shape(B, T, H, Hkv, d, q_ld, k_ld, v_ld, float(eps), float(theta or 0.0), _dtype_code(x.dtype)), dev
+    if wq is not None:
+        _dense("wq", wq, (d,), F32, dev)
+    if wk is not None:
+        _dense("wk", wk, (d,), F32, dev)
+    if pos is not None:
+        _dense("pos", pos, (B, T), INT32, dev)
+    return _qk_struct(B, T, H, Hkv, d, q_ld, k_ld, v_ld, float(eps), float(theta or 0.0), _dtype_code(dt)), dev, dt
+
+
+INT32 = (torch.int32,)
 
 
 def qk_norm_rope_fwd(q, k, wq=None, wk=None, *, pos=None, eps=1e-6, theta=500000.0, q_out=None, k_out=None,
@@ -663,20 +695,18 @@ def qk_norm_rope_fwd(q, k, wq=None, wk=None, *, pos=None, eps=1e-6, theta=500000
     """ua_qk_norm_rope_fwd: RMS norm of every head with the gains wq, wk [d] (None: no norm on that
     side) and the position rotation (theta 0: none), q [B,T,H,d] and k [B,T,Hkv,d] in one pass.  Either may
     be None; both may be slices of a fused projection's output.  Returns dict(q, k)."""
-    shape, dev = _qk_shape(q, k, wq, wk, pos, eps, theta)
+    shape, dev, dt = _qk_shape(q, k, wq, wk, pos, eps, theta)
     for name, x, y in (("q_out", q, q_out), ("k_out", k, k_out)):
-        if y is not None and x is None:
-            raise ValueError(f"{name}: given without its input")
-        if x is not None:
-            _dense(name, y, x.shape, (x.dtype,), dev)
+        if y is not None:
+            if x is None:
+                raise ValueError(f"{name}: given without its input")
+            _dense(name, y, x.shape, (dt,), dev)
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        q_out = _like(q)
     if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-    with torch.cuda.device(dev):
-        _check("ua_qk_norm_rope_fwd", load_library().ua_qk_norm_rope_fwd(
-            ctypes.byref(shape), _addr(q), _addr(k), _addr(wq), _addr(wk), _addr(pos), _addr(q_out), _addr(k_out),
-            _raw_stream(stream, dev)))
+        k_out = _like(k)
+    _launch("ua_qk_norm_rope_fwd", dev, load_library().ua_qk_norm_rope_fwd, ctypes.byref(shape), _addr(q), _addr(k),
+            _addr(wq), _addr(wk), _addr(pos), _addr(q_out), _addr(k_out), _raw_stream(stream, dev))
     return {"q": q_out, "k": k_out}
 
 
@@ -690,26 +720,25 @@ def qk_norm_rope_bwd_workspace_size(shape: ua_qk_shape) -> int:
 def qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, *, pos=None, eps=1e-6, theta=500000.0, ws=None, stream=None):
     """ua_qk_norm_rope_bwd: gradients of the forward with the same arguments.  Returns dict(dq, dk,
     dwq, dwk), None for what the forward did not have."""
-    shape, dev = _qk_shape(q, k, wq, wk, pos, eps, theta)
+    shape, dev, dt = _qk_shape(q, k, wq, wk, pos, eps, theta)
     for name, x, y in (("dq_out", q, dq_out), ("dk_out", k, dk_out)):
         if (x is None) != (y is None):
             raise ValueError(f"{name}: needed with its input, and only with it")
         if x is not None:
-            _dense(name, y, x.shape, (x.dtype,), dev)
+            _dense(name, y, x.shape, (dt,), dev)
     need = qk_norm_rope_bwd_workspace_size(shape)
     if ws is None or _nbytes(ws) < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    if ws.device != dev or not ws.is_contiguous():
+        ws = (q if q is not None else k).new_empty(need, dtype=torch.uint8)
+    elif ws.device != dev or not ws.is_contiguous():
         raise ValueError("ws: a contiguous tensor on the call's device is needed")
-    like = lambda x: None if x is None else torch.empty(x.shape, dtype=x.dtype, device=dev)  # noqa: E731
-    gr = {"dq": like(q), "dk": like(k), "dwq": like(wq) if q is not None else None,
-          "dwk": like(wk) if k is not None else None}
-    with torch.cuda.device(dev):
-        _check("ua_qk_norm_rope_bwd", load_library().ua_qk_norm_rope_bwd(
-            ctypes.byref(shape), _addr(q), _addr(k), _addr(wq), _addr(wk), _addr(pos), _addr(dq_out), _addr(dk_out),
-            _addr(gr["dq"]), _addr(gr["dk"]), _addr(gr["dwq"]), _addr(gr["dwk"]), ws.data_ptr(), _nbytes(ws),
-            _raw_stream(stream, dev)))
-    return gr
+    dq = None if q is None else _like(q)
+    dk = None if k is None else _like(k)
+    dwq = None if q is None or wq is None else torch.empty_like(wq)
+    dwk = None if k is None or wk is None else torch.empty_like(wk)
+    _launch("ua_qk_norm_rope_bwd", dev, load_library().ua_qk_norm_rope_bwd, ctypes.byref(shape), _addr(q), _addr(k),
+            _addr(wq), _addr(wk), _addr(pos), _addr(dq_out), _addr(dk_out), _addr(dq), _addr(dk), _addr(dwq),
+            _addr(dwk), ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
+    return {"dq": dq, "dk": dk, "dwq": dwq, "dwk": dwk}
 
 
 KVQ_FORMATS = {torch.int8: UA_KVQ_INT8, torch.float8_e4m3fn: UA_KVQ_E4M3}
@@ -765,11 +794,13 @@ class KVQCache:
                 raise ValueError(f"page_size {ps} must be a power of two >= 128 that divides the capacity {self.capacity}")
             _dense("cache.page_table", self.page_table, (self.B, max_pages), (torch.int32,), dev)
         paged = self.page_table is not None
-        object.__setattr__(self, "_struct", ua_kvq(
+        struct = ua_kvq(
             self.B, self.Hkv, self.d, self.capacity, _dtype_code(self.dtype), KVQ_FORMATS[self.k.dtype],
             *[t.data_ptr() for t in (self.k, self.v, self.k_scale, self.v_scale, self.k_ring, self.v_ring, self.n_kept,
                                      self.ring_state)],
-            ps if paged else 0, max_pages, pages if paged else 0, self.page_table.data_ptr() if paged else None))
+            ps if paged else 0, max_pages, pages if paged else 0, self.page_table.data_ptr() if paged else None)
+        object.__setattr__(self, "_ref", ctypes.byref(struct))   # (keeps the struct)
+        object.__setattr__(self, "device", dev)
 
     @staticmethod
     def _tensors(B, Hkv, d, pages, page_size, dtype, fmt, device):
@@ -813,24 +844,25 @@ def kvq_append(cache: KVQCache, k, v, q=None, *, wq=None, wk=None, pos=None, n_n
     the queries are normalised (wq) and rotated in the same launch and returned."""
     if k is None or v is None:
         raise ValueError("k and v are needed")
-    shape, dev = _qk_shape(q, k, wq, wk, pos, eps, theta, v)
-    if (shape.B, shape.Hkv, shape.d, k.dtype) != (cache.B, cache.Hkv, cache.d, cache.dtype):
-        raise ValueError(f"k: shape {tuple(k.shape)}, {k.dtype}, expected [{cache.B}, T, {cache.Hkv}, {cache.d}], {cache.dtype}")
-    if dev != cache.k.device:
-        raise ValueError(f"k: on {dev}, the cache is on {cache.k.device}")
-    _dense("n_new", n_new, (shape.B,), (torch.int32,), dev)
-    _dense("start", start, (shape.B,), (torch.int32,), dev)
+    shape, dev, dt = _qk_shape(q, k, wq, wk, pos, eps, theta, v)
+    if shape.B != cache.B or shape.Hkv != cache.Hkv or shape.d != cache.d or dt != cache.dtype:
+        raise ValueError(f"k: shape {tuple(k.shape)}, {dt}, expected [{cache.B}, T, {cache.Hkv}, {cache.d}], {cache.dtype}")
+    if dev != cache.device:
+        raise ValueError(f"k: on {dev}, the cache is on {cache.device}")
+    if n_new is not None:
+        _dense("n_new", n_new, cache.n_kept.shape, INT32, dev)
+    if start is not None:
+        _dense("start", start, cache.n_kept.shape, INT32, dev)
     if q is None:
         if q_out is not None:
             raise ValueError("q_out: given without its input")
     elif q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        q_out = _like(q)
     else:
-        _dense("q_out", q_out, q.shape, (q.dtype,), dev)
-    with torch.cuda.device(dev):
-        _check("ua_kvq_append", load_library().ua_kvq_append(
-            ctypes.byref(cache._struct), ctypes.byref(shape), _addr(q), k.data_ptr(), v.data_ptr(), _addr(wq), _addr(wk),
-            _addr(pos), _addr(n_new), _addr(start), _addr(q_out), _raw_stream(stream, dev)))
+        _dense("q_out", q_out, q.shape, (dt,), dev)
+    _launch("ua_kvq_append", dev, load_library().ua_kvq_append, cache._ref, ctypes.byref(shape), _addr(q), k.data_ptr(),
+            v.data_ptr(), _addr(wq), _addr(wk), _addr(pos), _addr(n_new), _addr(start), _addr(q_out),
+            _raw_stream(stream, dev))
     return q_out
 
 
@@ -838,7 +870,7 @@ def kvq_attend_workspace_size(cache: KVQCache, H: int, Tq: int = 1) -> int:
     """ua_kvq_attend_workspace_size: bytes of the attention's workspace (zeroed once, see alloc_workspace)."""
     n = ctypes.c_size_t(0)
     _check("ua_kvq_attend_workspace_size", load_library().ua_kvq_attend_workspace_size(
-        ctypes.byref(cache._struct), int(H), int(Tq), ctypes.byref(n)))
+        cache._ref, int(H), int(Tq), ctypes.byref(n)))
     return n.value
 
 
@@ -850,28 +882,32 @@ def kvq_attend(cache: KVQCache, q, *, g=None, bias=None, n_q=None, scale=None, o
     one is made without it).  Returns o, shaped like q."""
     if q.dim() not in (3, 4):
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [B, H, d] or [B, Tq, H, d]")
-    dev = cache.k.device
-    B, Tq, H, d = q.shape if q.dim() == 4 else (q.shape[0], 1, q.shape[1], q.shape[2])
-    if (B, d) != (cache.B, cache.d):
-        raise ValueError(f"q: shape {tuple(q.shape)}, expected [{cache.B}, Tq, H, {cache.d}]")
-    act = (cache.dtype,)
-    _dense("q", q, q.shape, act, dev)
-    _dense("g", g, q.shape, act, dev)
-    _dense("bias", bias, (B, cache.Hkv, cache.capacity), F32, dev)
-    _dense("n_q", n_q, (B,), (torch.int32,), dev)
-    _dense("out", out, q.shape, act, dev)
-    _dense("lse", lse, (B, H, Tq), F32, dev)
-    o = out if out is not None else torch.empty(q.shape, dtype=q.dtype, device=dev)
+    dev, dt, qs = cache.device, cache.dtype, q.shape
+    B, Tq, H, d = qs if len(qs) == 4 else (qs[0], 1, qs[1], qs[2])
+    if B != cache.B or d != cache.d:
+        raise ValueError(f"q: shape {tuple(qs)}, expected [{cache.B}, Tq, H, {cache.d}]")
+    act = (dt,)
+    _dense("q", q, qs, act, dev)
+    if g is not None:
+        _dense("g", g, qs, act, dev)
+    if bias is not None:
+        _dense("bias", bias, (B, cache.Hkv, cache.capacity), F32, dev)
+    if n_q is not None:
+        _dense("n_q", n_q, (B,), INT32, dev)
+    if lse is not None:
+        _dense("lse", lse, (B, H, Tq), F32, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _dense("out", out, qs, act, dev)
     if ws is None:
         ws = alloc_workspace(kvq_attend_workspace_size(cache, H, Tq), dev)
-    if ws.device != dev or not ws.is_contiguous():
+    elif ws.device != dev or not ws.is_contiguous():
         raise ValueError("ws: a contiguous tensor on the call's device is needed")
-    with torch.cuda.device(dev):
-        _check("ua_kvq_attend", load_library().ua_kvq_attend(
-            ctypes.byref(cache._struct), H, Tq, q.data_ptr(), _addr(g), _addr(bias), _addr(n_q),
-            float(d) ** -0.5 if scale is None else float(scale), o.data_ptr(), _addr(lse), ws.data_ptr(), _nbytes(ws),
-            _raw_stream(stream, dev)))
-    return o
+    _launch("ua_kvq_attend", dev, load_library().ua_kvq_attend, cache._ref, H, Tq, q.data_ptr(), _addr(g), _addr(bias),
+            _addr(n_q), float(d) ** -0.5 if scale is None else float(scale), out.data_ptr(), _addr(lse), ws.data_ptr(),
+            _nbytes(ws), _raw_stream(stream, dev))
+    return out
 
 
 def get_device_status(stream=None) -> int:
