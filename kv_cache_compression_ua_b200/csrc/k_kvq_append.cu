@@ -8,8 +8,6 @@
 // CH = DH/16 lanes a row, every element of the block in registers between the one read and the
 // write of its code, so the block's largest magnitude costs one reduction and no second read.
 // The thread's eight angles are formed once and serve all hpc heads.
-#include <cuda_fp8.h>
-
 #include "qk_norm.cuh"
 #include "ua_profile.h"
 
@@ -66,20 +64,29 @@ template <bool E4M3> __device__ __forceinline__ float block_scale(uint32_t amax_
 // 8 codes of a row's chunk
 template <typename T, bool E4M3> __device__ __forceinline__ uint2 encode8(const Raw8<T>& raw, float factor) {
     if (factor == 0.f) return make_uint2(0, 0);
+    F2 y[4];
     float x[8];
-    raw.get(x);
-    uint32_t w[2] = {0, 0};
+    raw.get(y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], f2(factor, factor));
+    unpairs(y, x);
+    uint32_t w[2];
     if constexpr (E4M3) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * factor, x[2 * i + 1] * factor),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            w[i / 2] |= c2 << (16 * (i & 1));
-        }
+        for (int i = 0; i < 2; ++i)
+            asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+                "mov.b32 %0, {l, h};\n\t}"
+                : "=r"(w[i])
+                : "f"(x[4 * i]), "f"(x[4 * i + 1]), "f"(x[4 * i + 2]), "f"(x[4 * i + 3]));
     } else {
+        // |x * factor| <= 127 (1 + 2^-23): rounds to 127 at most.  1.5 * 2^23 more leaves the rounded
+        // (to even) number in the low byte.
 #pragma unroll
-        for (int i = 0; i < 8; ++i)               // |x * factor| <= 127 (1 + 2^-23): rounds to 127 at most
-            w[i / 4] |= (uint32_t)(__float2int_rn(x[i] * factor) & 0xff) << (8 * (i & 3));
+        for (int i = 0; i < 8; ++i) x[i] += 12582912.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = __byte_perm(__byte_perm(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]), 0x0040),
+                               __byte_perm(__float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3]), 0x0040), 0x5410);
     }
     return make_uint2(w[0], w[1]);
 }
@@ -97,7 +104,7 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
     extern __shared__ __align__(16) unsigned char s_queue[];
     __shared__ __align__(16) float s_cos[TOK * HALF], s_sin[TOK * HALF];
     __shared__ double s_f[HALF];
-    __shared__ uint32_t s_max[2][2][NW];
+    __shared__ __align__(16) uint32_t s_max[2][2][NW];   // the warps' largest magnitudes, keys and values
     __shared__ int s_last;
     grid_dep_wait();
     grid_dep_release();
@@ -184,12 +191,37 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
 #pragma unroll
                 for (int i = 0; i < DEPTH - 1; ++i) fetch(i, i);
                 const long long crow = full ? kvq_row(p.c, b, blk) : -1;
-                F2 cs[4], sn[4], ns[4];
-                if (p.n.rope && is_new) {
-                    const int pos = p.n.pos ? p.n.pos[n] : slot;
-                    lane_angles<T>(pos, s_f, c, cs, sn);
-                    negate(sn, ns);
+                // The gain and the rotation of a token's pairs together, the same for every head:
+                // (a0, a1) -> r (a0 w0 cos - a1 w1 sin, a1 w1 cos + a0 w0 sin), r the head's own.
+                F2 c00[4], c01[4], c11[4], c10[4];
+                if (is_new && p.n.rope) {
+                    F2 cs[4], sn[4];
+                    lane_angles<T>(p.n.pos ? p.n.pos[n] : slot, s_f, c, cs, sn);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        c00[i] = c11[i] = cs[i];
+                        c01[i] = neg2(sn[i]);
+                        c10[i] = sn[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        c00[i] = c11[i] = f2(1.f, 1.f);
+                        c01[i] = c10[i] = f2(0.f, 0.f);
+                    }
                 }
+                if (p.n.wk != nullptr) {
+                    F2 w0[4], w1[4];
+                    load_gains<DH>(p.n.wk, c, w0, w1);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        c00[i] = mul2(c00[i], w0[i]);
+                        c10[i] = mul2(c10[i], w0[i]);
+                        c01[i] = mul2(c01[i], w1[i]);
+                        c11[i] = mul2(c11[i], w1[i]);
+                    }
+                }
+                const bool changed = p.n.wk != nullptr || p.n.rope;
                 int stage = 0;
 #pragma unroll 1
                 for (int hh = 0; hh < p.hpc; ++hh) {
@@ -201,17 +233,22 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
                         ka.u[i] = queue.get(stage, i);
                         kb.u[i] = queue.get(stage, NV + i);
                     }
-                    if (p.n.wk != nullptr || p.n.rope) {
+                    if (changed) {
                         F2 x0[4], x1[4];
                         ka.get(x0);
                         kb.get(x1);
+                        F2 r2 = f2(1.f, 1.f);
                         if (p.n.wk != nullptr) {
-                            F2 w0[4], w1[4];
-                            load_gains<DH>(p.n.wk, c, w0, w1);
-                            norm_row<DH>(x0, x1, w0, w1, p.n.eps);
+                            const float r = row_rstd<DH>(x0, x1, p.n.eps);
+                            r2 = f2(r, r);
                         }
                         if (is_new) {                    // rounded to the activation type: codes are formed
-                            if (p.n.rope) rotate_row(x0, x1, cs, sn, ns);       // from what the ring would hold
+#pragma unroll                                           // from what the ring would hold
+                            for (int i = 0; i < 4; ++i) {
+                                const F2 a = mul2(x0[i], r2), b2 = mul2(x1[i], r2);
+                                x0[i] = fma2(b2, c01[i], mul2(a, c00[i]));
+                                x1[i] = fma2(a, c10[i], mul2(b2, c11[i]));
+                            }
                             ka.put(x0);
                             kb.put(x1);
                         }
@@ -223,17 +260,19 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
                     }
                     stage = (stage + 1) % DEPTH;
                     if (full) {
-                        uint32_t mk = __reduce_max_sync(0xffffffffu, max(ka.amax_bits(), kb.amax_bits()));
-                        uint32_t mv = __reduce_max_sync(0xffffffffu, max(va.amax_bits(), vb.amax_bits()));
+                        uint32_t mk = __reduce_max_sync(0xffffffffu, ka.amax_bits(kb));
+                        uint32_t mv = __reduce_max_sync(0xffffffffu, va.amax_bits(vb));
                         if ((tid & 31) == 0) {
                             s_max[buf][0][tid >> 5] = mk;
                             s_max[buf][1][tid >> 5] = mv;
                         }
                         __syncthreads();                 // (also: this head's earlier rows have been read from the ring)
 #pragma unroll
-                        for (int i = 0; i < NW; ++i) {
-                            mk = max(mk, s_max[buf][0][i]);
-                            mv = max(mv, s_max[buf][1][i]);
+                        for (int i = 0; i < NW; i += 4) {
+                            const uint4 a = *reinterpret_cast<const uint4*>(&s_max[buf][0][i]);
+                            const uint4 b4 = *reinterpret_cast<const uint4*>(&s_max[buf][1][i]);
+                            mk = max(max(mk, max(a.x, a.y)), max(a.z, a.w));
+                            mv = max(max(mv, max(b4.x, b4.y)), max(b4.z, b4.w));
                         }
                         buf ^= 1;
                         if (crow >= 0) {

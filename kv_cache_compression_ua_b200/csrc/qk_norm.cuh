@@ -94,20 +94,31 @@ template <typename T> struct Raw8 {
                                   __float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3]));
         }
     }
-    // bits of the largest magnitude (non-negative floats order as their bits, NaN last)
-    __device__ __forceinline__ uint32_t amax_bits() const {
+    // bits of the largest magnitude of this and another's (non-negative floats order as their bits, NaN
+    // above all)
+    __device__ __forceinline__ uint32_t amax_bits(const Raw8& o) const {
         if constexpr (NV == 1) {
-            const uint32_t m = 0x7fff7fffu;
-            const uint32_t a = __vmaxu2(__vmaxu2(u[0].x & m, u[0].y & m), __vmaxu2(u[0].z & m, u[0].w & m));
+            uint32_t a = amax2(amax2(amax2(u[0].x, u[0].y), amax2(u[0].z, u[0].w)),
+                               amax2(amax2(o.u[0].x, o.u[0].y), amax2(o.u[0].z, o.u[0].w)));
+            a &= 0x7fff7fffu;
             return max(a & 0xffff0000u, a << 16);
         } else {
             uint32_t a = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
                 a = max(max(a, max(u[i].x & 0x7fffffffu, u[i].y & 0x7fffffffu)),
                         max(u[i].z & 0x7fffffffu, u[i].w & 0x7fffffffu));
+                a = max(max(a, max(o.u[i].x & 0x7fffffffu, o.u[i].y & 0x7fffffffu)),
+                        max(o.u[i].z & 0x7fffffffu, o.u[i].w & 0x7fffffffu));
+            }
             return a;
         }
+    }
+    // larger magnitudes of two bf16 pairs, NaN kept; the signs are of no meaning
+    static __device__ __forceinline__ uint32_t amax2(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
     }
     __device__ __forceinline__ void st(T* p) const {
 #pragma unroll
@@ -137,13 +148,18 @@ template <int CH> __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-template <int DH> __device__ __forceinline__ void norm_row(F2* x0, F2* x1, const F2* w0, const F2* w1, float eps) {
+// 1 / sqrt(mean square + eps) of a head
+template <int DH> __device__ __forceinline__ float row_rstd(const F2* x0, const F2* x1, float eps) {
     F2 ss = mul2(x0[0], x0[0]);
 #pragma unroll
     for (int i = 1; i < 4; ++i) ss = fma2(x0[i], x0[i], ss);
 #pragma unroll
     for (int i = 0; i < 4; ++i) ss = fma2(x1[i], x1[i], ss);
-    const float r = rsqrtf(row_sum<DH / 16>(hsum(ss)) * (1.f / DH) + eps);
+    return rsqrtf(row_sum<DH / 16>(hsum(ss)) * (1.f / DH) + eps);
+}
+
+template <int DH> __device__ __forceinline__ void norm_row(F2* x0, F2* x1, const F2* w0, const F2* w1, float eps) {
+    const float r = row_rstd<DH>(x0, x1, eps);
     const F2 r2 = f2(r, r);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

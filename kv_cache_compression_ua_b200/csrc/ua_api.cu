@@ -1008,8 +1008,11 @@ ua_status ua_kvq_append(const ua_kvq* c, const ua_qk_shape* s, const void* q, co
     p.v_ld = s->v_ld ? s->v_ld : (long long)s->Hkv * s->d;
     p.n_new = n_new; p.start = start;
     p.nb = (int)(((long long)s->T + 2 * kKvqBlock - 2) / kKvqBlock);
-    // all KV heads in one CTA share a token's angles; fewer heads a CTA where the blocks alone leave SMs idle
-    p.hpc = s->Hkv;
+    // All KV heads in one CTA share a token's angles; fewer heads a CTA where the blocks alone leave SMs
+    // idle (3B chunk of 4 x 1003 tokens: one head each 30 us, two 22 us).  A step of less than a block
+    // has a row or a few a CTA and is latency: one head each (32 tokens of the 1B shape, cold: 7.3 us, two
+    // heads 9.4 us).
+    p.hpc = s->T < kKvqBlock ? 1 : s->Hkv;
     while (p.hpc > 1 && (long long)s->B * p.nb * (s->Hkv / p.hpc) < kAppendCtas) {
         int next = p.hpc - 1;
         while (s->Hkv % next) --next;
