@@ -85,15 +85,25 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t w) {       // one instructi
     asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(y) : "r"(w), "r"(keep), "r"(flip));
     return y;
 }
-template <bool E4M3> __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    if constexpr (E4M3) {
+// For fp32 results the sums would lose two bits to the 128 (fp32 drafts: 2e-5 against 5e-7): there the
+// byte is the mantissa of 1024 + (code + 128), and 1152 is subtracted at once.
+enum Kind { kE4m3, kInt8, kInt8Exact };
+template <Kind K> __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if constexpr (K == kE4m3) {
         asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
             "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
             : "=r"(lo), "=r"(hi)
             : "r"(w));
-    } else {
+    } else if constexpr (K == kInt8) {
         lo = and_xor(w);
         hi = and_xor(w >> 8);
+    } else {
+        w ^= 0x80808080u;
+        const __half2 off = __half2half2(__ushort_as_half(0x6480));        // 1152
+        uint32_t a = __byte_perm(w, 0x64646464u, 0x4240), b = __byte_perm(w, 0x64646464u, 0x4341);
+        __half2 ha = __hsub2(*reinterpret_cast<__half2*>(&a), off), hb = __hsub2(*reinterpret_cast<__half2*>(&b), off);
+        lo = *reinterpret_cast<uint32_t*>(&ha);
+        hi = *reinterpret_cast<uint32_t*>(&hb);
     }
 }
 // Bytes of two tokens' words so that codes_f16 pairs the tokens: elements 0, 1 (k = 0) or 2, 3 (k = 1)
@@ -149,6 +159,8 @@ __device__ __forceinline__ int o_place(int row, int el) { return el ^ (row & 6);
 
 template <typename T, int DH, int NT, bool E4M3> struct Att {
     static constexpr bool F32 = sizeof(T) == 4;
+    static constexpr Kind KIND = E4M3 ? kE4m3 : F32 ? kInt8Exact : kInt8;
+    static constexpr bool OFF = KIND == kInt8;       // codes enter the products with 128 added, times 2^-24
     static constexpr int R = 8 * NT;                 // query rows of a tile
     static constexpr int QP = F32 ? 2 : 1;           // f16 parts of a query
     static constexpr int PP = F32 ? 2 : 1;           // f16 parts of a probability
@@ -459,7 +471,7 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 qf[nt][e] = sm.qf[8 * nt + 2 * c + e];
-                s0[nt][e] = s0[nt][e + 2] = E4M3 ? 0.f : sm.s0[8 * nt + 2 * c + e];
+                s0[nt][e] = s0[nt][e + 2] = A::OFF ? sm.s0[8 * nt + 2 * c + e] : 0.f;
                 lim[nt][e] = sm.lim[8 * nt + 2 * c + e];
                 lim_min = min(lim_min, lim[nt][e]);
             }
@@ -522,8 +534,8 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     uint32_t a[4];
-                    codes_f16<E4M3>(w0[s], a[0], a[2]);
-                    codes_f16<E4M3>(w1[s], a[1], a[3]);
+                    codes_f16<A::KIND>(w0[s], a[0], a[2]);
+                    codes_f16<A::KIND>(w1[s], a[1], a[3]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -550,7 +562,7 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) f[nt][e] = E4M3 ? qf[nt][e] * ks : qf[nt][e] * ks * (1.f / kI8Unit);
+            for (int e = 0; e < 2; ++e) f[nt][e] = A::OFF ? qf[nt][e] * ks * (1.f / kI8Unit) : qf[nt][e] * ks;
         bool plain = bias0 == nullptr && blk * kKvqBlock + kKvqBlock - 1 <= lim_min && p.scale > 0.f;
         if (plain) {
             float mn[NT][2], base[NT][2];
@@ -622,7 +634,7 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
                     pb[1][mt][nt] = make_uint2(transpose8x8(pack_f16(x[mt][nt][0] - l2.x, x[mt][nt][1] - l2.y)),
                                                transpose8x8(pack_f16(x[mt][nt][2] - h2.x, x[mt][nt][3] - h2.y)));
                 }
-                if constexpr (!E4M3) {
+                if constexpr (A::OFF) {
                     if (mt == 0) mma_f16(sum[nt], ones, pb[0][mt][nt], none);
                     else mma_f16(sum[nt], ones, pb[0][mt][nt]);
                     if constexpr (A::PP == 2) mma_f16(sum[nt], ones, pb[1][mt][nt]);
@@ -639,9 +651,9 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
                 for (int mt = 1; mt < 4; ++mt) l += x[mt][nt][e] + x[mt][nt][e + 2];
                 st.l[nt][e] = fmaf(st.l[nt][e], corr[nt][e], l);
                 rescale = rescale || corr[nt][e] != 1.f;
-                o0[nt][e] = o0[nt][e + 2] = E4M3 ? 0.f : -128.f * kI8Unit * sum[nt][e];
+                o0[nt][e] = o0[nt][e + 2] = A::OFF ? -128.f * kI8Unit * sum[nt][e] : 0.f;
                 // (a block no slot of which is seen may have a NaN scale)
-                fv[nt][e] = any[nt][e] ? (E4M3 ? vs : vs * (1.f / kI8Unit)) : 0.f;
+                fv[nt][e] = any[nt][e] ? (A::OFF ? vs * (1.f / kI8Unit) : vs) : 0.f;
             }
         if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll
@@ -670,8 +682,8 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         uint32_t a[4];
-                        codes_f16<E4M3>(token_pair<E4M3>(t0, t1, k), a[0], a[1]);
-                        codes_f16<E4M3>(token_pair<E4M3>(t2, t3, k), a[2], a[3]);
+                        codes_f16<A::KIND>(token_pair<E4M3>(t0, t1, k), a[0], a[1]);
+                        codes_f16<A::KIND>(token_pair<E4M3>(t2, t3, k), a[2], a[3]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -724,31 +736,37 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
         *units = Hkv * tiles_of(nq);
         return *units * (blocks_of(n) + kUnitCost);
     };
-    // all items and units (below 2^31: checked on the host)
-    int total = 0, units = 0;
-    for (int b = tid; b < p.c.B; b += kThreads) {
-        int u;
-        total += items_of(b, &u);
-        units += u;
+    // All items and units (below 2^31: checked on the host).  Up to 32 sequences: every warp for itself,
+    // a sequence a lane.
+    const bool few = p.c.B <= 32;
+    int total = 0, units = 0, my_units = 0, my_blocks = 0;
+    for (int b = few ? lane : tid; b < p.c.B; b += few ? 32 : kThreads) {
+        total += items_of(b, &my_units);
+        units += my_units;
     }
+    if (few && my_units > 0) my_blocks = total / my_units - kUnitCost;
     total = __reduce_add_sync(0xffffffffu, total);
     units = __reduce_add_sync(0xffffffffu, units);
-    if (lane == 0) {
-        sm.scan[0][warp] = total;
-        sm.scan[1][warp] = units;
-    }
-    __syncthreads();
-    total = units = 0;
+    if (!few) {
+        if (lane == 0) {
+            sm.scan[0][warp] = total;
+            sm.scan[1][warp] = units;
+        }
+        __syncthreads();
+        total = units = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        total += sm.scan[0][w];
-        units += sm.scan[1][w];
+        for (int w = 0; w < kWarps; ++w) {
+            total += sm.scan[0][w];
+            units += sm.scan[1][w];
+        }
     }
-    // Equal runs of items, one a CTA.
-    int ctas = max(min(units, (int)gridDim.x), min((int)gridDim.x, (total + A::kMinItems - 1) / A::kMinItems));
-    if (units > 0 && ctas % units * 4 <= ctas) ctas -= ctas % units;    // units of one length: they start where a run starts
-    const int cta = blockIdx.x;
-    if (cta >= ctas) return;
+    const int cta = blockIdx.x, grid = gridDim.x;
+    // Few units: whole CTAs for each, `run` blocks each at most -- a CTA with parts of two units would
+    // pay for starting and merging twice (3B decode with bias: 29 us; 21 us so).
+    const bool aligned = few && units * 2 <= grid;
+    // Otherwise equal runs of items, one a CTA.
+    const int ctas = max(min(units, grid), min(grid, (total + A::kMinItems - 1) / A::kMinItems));
+    if (!aligned && cta >= ctas) return;
     // floor(a * b / c) for products below 2^53 (the quotient's fraction is at least 1 / c off a whole number)
     auto run_start = [&](int k) { return (int)((double)k * (double)total / (double)ctas); };
     auto run_of = [&](int item) { return (int)((((double)item + 1.0) * ctas - 1.0) / total); };
@@ -759,8 +777,8 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
     struct Segment {
         int b, h, rt, nq, n, nb, k0, k1, r_lo, r_hi, off, len;
     };
-    int at = run_start(cta);
-    const int hi = run_start(cta + 1);
+    int at = aligned ? 0 : run_start(cta);
+    const int hi = aligned ? 0 : run_start(cta + 1);
     // the segment that starts with item `at`, item `off` of sequence b
     auto segment = [&](int b, int off) {
         Segment s;
@@ -803,6 +821,44 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
             first += __shfl_sync(0xffffffffu, inc, 31);
         }
     };
+    // Whole CTAs for each unit: the least of 32 ascending numbers of blocks a CTA (by a sixteenth
+    // of the even share) with which the units need no more CTAs than there are; this CTA's part.
+    auto own_part = [&](bool* have) {
+        const int blocks = __reduce_add_sync(0xffffffffu, my_units * my_blocks);
+        const int even = max((blocks + grid - 1) / grid, kWarps), mine = even + even * lane / 16 + lane;
+        int need = 0;
+        for (int b = 0; b < p.c.B; ++b) {
+            const int nb = __shfl_sync(0xffffffffu, my_blocks, b);
+            need += __shfl_sync(0xffffffffu, my_units, b) * ((nb + mine - 1) / mine);
+        }
+        const unsigned fits = __ballot_sync(0xffffffffu, need <= grid);
+        const int run = __shfl_sync(0xffffffffu, mine, __ffs(fits) - 1);
+        const int parts = (my_blocks + run - 1) / run;   // CTAs a unit, of this lane's sequence
+        int inc = my_units * parts;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, cta < inc);
+        Segment s = {};
+        *have = past != 0;
+        if (!past) return s;
+        const int l = __ffs(past) - 1, k = __shfl_sync(0xffffffffu, parts, l);
+        const int off = cta - __shfl_sync(0xffffffffu, inc - my_units * parts, l), u = off / k, part = off - u * k;
+        s.b = l;
+        counts(l, &s.nq, &s.n);
+        s.nb = blocks_of(s.n);
+        const int tiles = tiles_of(s.nq);
+        s.h = u / tiles;
+        s.rt = u - s.h * tiles;
+        s.k0 = (int)((long long)part * s.nb / k);
+        s.k1 = (int)((long long)(part + 1) * s.nb / k);
+        s.r_lo = cta - part;
+        s.r_hi = s.r_lo + k - 1;
+        s.off = s.len = 0;
+        return s;
+    };
     Walk<T, DH, NT, E4M3> walk(p, sm);
     // Queries of a tile: 8 threads a row, fetched before the segment's copies are started so that
     // they need not queue behind them.
@@ -823,7 +879,9 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
         const int nfull = s.n / kKvqBlock;
         walk.begin(s.b, s.h, s.k0 + warp, min(s.k1, nfull), s.k1 == s.nb, s.n);
     };
-    Segment cur = find();
+    bool have = true;
+    Segment cur = aligned ? own_part(&have) : find();
+    if (!have) return;
     start(cur);
     for (;;) {
         const int h = cur.h, rt = cur.rt, nq = cur.nq, n = cur.n, b = cur.b, r_lo = cur.r_lo, r_hi = cur.r_hi;
@@ -993,8 +1051,10 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
                 const unsigned at_ = atomicAdd(cnt, 1u);
                 sm.last = at_ == (unsigned)(r_hi - r_lo);
                 if (at_ > (unsigned)(r_hi - r_lo)) raise_status(UA_ERR_INVALID_ARG);  // not zeroed
-                if (sm.last) *cnt = 0;
-                __threadfence();
+                if (sm.last) {
+                    *cnt = 0;
+                    __threadfence();
+                }
             }
             __syncthreads();
             if (sm.last) {

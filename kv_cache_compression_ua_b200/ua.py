@@ -614,15 +614,13 @@ def _heads(name, t, B, T, d, dtype, dev):
     """Checks an input [B, T, heads, d] whose tokens' heads are contiguous (a dense tensor, or a slice
     of a fused projection's output) and returns (heads, elements between tokens; 0: dense)."""
     s = t.shape
-    if len(s) != 4 or s[0] != B or s[1] != T or s[3] != d:
+    n = s[2] if len(s) == 4 else 0
+    if s != (B, T, n, d):
         raise ValueError(f"{name}: shape {tuple(s)}, expected [{B}, {T}, heads, {d}]")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.device != dev:
         raise ValueError(f"{name}: on {t.device}, the call runs on {dev}")
-    if not t.is_cuda:
-        raise ValueError("libua takes CUDA tensors")
-    n = s[2]
     if t.is_contiguous():
         return n, 0
     sb, st, sh, se = t.stride()
@@ -641,7 +639,13 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without building a Stream object (2 us of a 10 us call)
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(stream, dev):
+    if stream is None and _current_raw is not None:
+        return _current_raw(dev.index)
     return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
 
 
@@ -671,6 +675,8 @@ def _qk_shape(q, k, wq, wk, pos, eps, theta, v=None):
         raise ValueError(f"q or k: shape {tuple(x.shape)}, expected [B, T, heads, d]")
     B, T, _, d = x.shape
     dev, dt = x.device, x.dtype
+    if dev.type != "cuda":
+        raise ValueError("libua takes CUDA tensors")
     H, q_ld = _heads("q", q, B, T, d, dt, dev) if q is not None else (1, 0)
     Hkv, k_ld = _heads("k", k, B, T, d, dt, dev) if k is not None else (1, 0)
     v_ld = 0

@@ -123,10 +123,10 @@ def rows_of(cache, which, b, h, n):
 
 
 def offsets_of(cache, which, b, h, n):
-    """[n, 1]: 128 scales of an int8 slot: its products are formed with code + 128, so the rounding of their sums
-    is relative to |value| + 128 scales.  0 for e4m3 and for rows in the ring."""
+    """[n, 1]: 128 scales of an int8 slot of a bf16 cache: its products are formed with code + 128, so the rounding of
+    their sums is relative to |value| + 128 scales.  0 for e4m3, for fp32 and for rows in the ring."""
     out = torch.zeros(n, 1, dtype=torch.float64)
-    if cache.k.dtype == torch.int8:
+    if cache.k.dtype == torch.int8 and cache.dtype == torch.bfloat16:
         sc = cache.k_scale if which == "k" else cache.v_scale
         for blk in range(n // BLOCK):
             pg = b if cache.page_table is None else int(cache.page_table[b, blk * BLOCK // cache.page_size])
@@ -142,7 +142,8 @@ def attend(cache, q, n, *, g=None, bias=None, n_q=None, scale=None):
     logit's.  A logit off by e moves every probability by a factor within e; probabilities are f16 (2^-11) or,
     for fp32, two f16 parts (2^-22), exp2 is off by 2^-22 and its argument's rounding by 2^-23 |x - m|,
     the sums by the number of their terms in a lane: 64 half steps + 20 for each merge.  The weighted values'
-    sums round 4 times a block and once for the offset, by up to a whole step of |value| + offset: 24 half steps."""
+    sums round 4 times a block and once for the offset, by up to a whole step of |value| + offset: 24 half steps
+    (the offset: see offsets_of)."""
     B, Tq, H, d = q.shape
     Hkv = cache.Hkv
     G = H // Hkv
