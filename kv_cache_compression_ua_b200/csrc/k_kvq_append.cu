@@ -91,6 +91,16 @@ template <typename T, bool E4M3> __device__ __forceinline__ uint2 encode8(const 
     return make_uint2(w[0], w[1]);
 }
 
+// ... to where the chunk's pieces lie
+template <typename T, int DH> __device__ __forceinline__ void put_codes(uint8_t* d, uint2 w) {
+    if constexpr (Raw8<T>::NV == 1) {
+        *reinterpret_cast<uint2*>(d) = w;
+    } else {
+        *reinterpret_cast<uint32_t*>(d) = w.x;
+        *reinterpret_cast<uint32_t*>(d + kPieceStep<T, DH>) = w.y;
+    }
+}
+
 // grid: B * (Hkv / hpc) * nb block CTAs, then q_tiles * q_split query CTAs; 4 * DH threads
 template <typename T> struct KvQueue {
     static constexpr int NV = Raw8<T>::NV, DEPTH = 2;
@@ -162,14 +172,14 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
                 const bool is_new = t >= 0 && slot < end, old = full && t < 0;
                 const int n = b * T_ + t;
                 // this thread's chunk in the ring, of head h: ring + h * kKvqRing * DH
-                const size_t ring = (((size_t)b * Hkv + gi * p.hpc) * kKvqRing + (slot & (kKvqRing - 1))) * DH + 8 * c;
+                const size_t ring = (((size_t)b * Hkv + gi * p.hpc) * kKvqRing + (slot & (kKvqRing - 1))) * DH + lane_at<T>(c);
                 T* kr = static_cast<T*>(p.c.kr) + ring;
                 T* vr = static_cast<T*>(p.c.vr) + ring;
                 const T* ksrc = old ? kr : static_cast<const T*>(p.n.k);
                 const T* vsrc = old ? vr : static_cast<const T*>(p.v);
                 if (is_new) {
-                    ksrc += (long long)n * p.n.k_ld + gi * p.hpc * DH + 8 * c;
-                    vsrc += (long long)n * p.v_ld + gi * p.hpc * DH + 8 * c;
+                    ksrc += (long long)n * p.n.k_ld + gi * p.hpc * DH + lane_at<T>(c);
+                    vsrc += (long long)n * p.v_ld + gi * p.hpc * DH + lane_at<T>(c);
                 }
                 const int hstep = old ? kKvqRing * DH : DH;
                 auto fetch = [&](int hh, int stage) {
@@ -179,10 +189,10 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
                             const T* v = vsrc + hh * hstep;
 #pragma unroll
                             for (int i = 0; i < NV; ++i) {
-                                queue.put(stage, i, k + i * Vec16<T>::N);
-                                queue.put(stage, NV + i, k + HALF + i * Vec16<T>::N);
-                                queue.put(stage, 2 * NV + i, v + i * Vec16<T>::N);
-                                queue.put(stage, 3 * NV + i, v + HALF + i * Vec16<T>::N);
+                                queue.put(stage, i, k + i * kPieceStep<T, DH>);
+                                queue.put(stage, NV + i, k + HALF + i * kPieceStep<T, DH>);
+                                queue.put(stage, 2 * NV + i, v + i * kPieceStep<T, DH>);
+                                queue.put(stage, 3 * NV + i, v + HALF + i * kPieceStep<T, DH>);
                             }
                         }
                     }
@@ -196,7 +206,7 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
                 F2 c00[4], c01[4], c11[4], c10[4];
                 if (is_new && p.n.rope) {
                     F2 cs[4], sn[4];
-                    lane_angles<T>(p.n.pos ? p.n.pos[n] : slot, s_f, c, cs, sn);
+                    lane_angles<T, DH>(p.n.pos ? p.n.pos[n] : slot, s_f, c, cs, sn);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         c00[i] = c11[i] = cs[i];
@@ -212,7 +222,7 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
                 }
                 if (p.n.wk != nullptr) {
                     F2 w0[4], w1[4];
-                    load_gains<DH>(p.n.wk, c, w0, w1);
+                    load_gains<T, DH>(p.n.wk, c, w0, w1);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         c00[i] = mul2(c00[i], w0[i]);
@@ -279,12 +289,12 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
                             const long long r = crow + (long long)(gi * p.hpc + hh) * p.c.bpp;
                             float fk, fv;
                             const float sk = block_scale<E4M3>(mk, &fk), sv = block_scale<E4M3>(mv, &fv);
-                            uint8_t* dk = p.c.k + r * (kKvqBlock * DH) + row * DH + 8 * c;
-                            uint8_t* dv = p.c.v + r * (kKvqBlock * DH) + row * DH + 8 * c;
-                            *reinterpret_cast<uint2*>(dk) = encode8<T, E4M3>(ka, fk);
-                            *reinterpret_cast<uint2*>(dk + HALF) = encode8<T, E4M3>(kb, fk);
-                            *reinterpret_cast<uint2*>(dv) = encode8<T, E4M3>(va, fv);
-                            *reinterpret_cast<uint2*>(dv + HALF) = encode8<T, E4M3>(vb, fv);
+                            uint8_t* dk = p.c.k + r * (kKvqBlock * DH) + row * DH + lane_at<T>(c);
+                            uint8_t* dv = p.c.v + r * (kKvqBlock * DH) + row * DH + lane_at<T>(c);
+                            put_codes<T, DH>(dk, encode8<T, E4M3>(ka, fk));
+                            put_codes<T, DH>(dk + HALF, encode8<T, E4M3>(kb, fk));
+                            put_codes<T, DH>(dv, encode8<T, E4M3>(va, fv));
+                            put_codes<T, DH>(dv + HALF, encode8<T, E4M3>(vb, fv));
                             if (tid == 0) {
                                 p.c.ks[r] = sk;
                                 p.c.vs[r] = sv;
@@ -294,8 +304,8 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
                     if (is_new && keep) {
                         T* kd = kr + (size_t)hh * kKvqRing * DH;
                         T* vd = vr + (size_t)hh * kKvqRing * DH;
-                        ka.st(kd); kb.st(kd + HALF);
-                        va.st(vd); vb.st(vd + HALF);
+                        ka.template st<DH>(kd); kb.template st<DH>(kd + HALF);
+                        va.template st<DH>(vd); vb.template st<DH>(vd + HALF);
                     }
                 }
                 queue.template wait<0>();

@@ -58,8 +58,8 @@ __device__ __forceinline__ void bwd_run(const QkNormParams& p, bool is_q, int ct
     typename BwdQueue<T>::Queue queue(s_queue);
     // the next item to fetch: its place in dy (and dx) and in x
     int left = count, fi = lo % quads, fn = lo / quads * TOK + row / kNormHeads, fstage = 0;
-    const T* fg = dy + ((long long)fn * nh + fi * kNormHeads + hp) * DH + 8 * c;
-    const T* fx = static_cast<const T*>(is_q ? p.q : p.k) + fn * ld + (fi * kNormHeads + hp) * DH + 8 * c;
+    const T* fg = dy + ((long long)fn * nh + fi * kNormHeads + hp) * DH + lane_at<T>(c);
+    const T* fx = static_cast<const T*>(is_q ? p.q : p.k) + fn * ld + (fi * kNormHeads + hp) * DH + lane_at<T>(c);
     const long long g_jump = ((long long)TOK * nh - (quads - 1) * kNormHeads) * DH;   // from a tile's last quad to the
     const long long x_jump = TOK * ld - (long long)(quads - 1) * kNormHeads * DH;     // next tile's first
     auto fetch = [&]() {
@@ -68,11 +68,11 @@ __device__ __forceinline__ void bwd_run(const QkNormParams& p, bool is_q, int ct
             if (fn < N && fi * kNormHeads + hp < nh) {
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    queue.put(fstage, v, fg + v * Vec16<T>::N);
-                    queue.put(fstage, NV + v, fg + HALF + v * Vec16<T>::N);
+                    queue.put(fstage, v, fg + v * kPieceStep<T, DH>);
+                    queue.put(fstage, NV + v, fg + HALF + v * kPieceStep<T, DH>);
                     if (NORM) {
-                        queue.put(fstage, 2 * NV + v, fx + v * Vec16<T>::N);
-                        queue.put(fstage, 3 * NV + v, fx + HALF + v * Vec16<T>::N);
+                        queue.put(fstage, 2 * NV + v, fx + v * kPieceStep<T, DH>);
+                        queue.put(fstage, 3 * NV + v, fx + HALF + v * kPieceStep<T, DH>);
                     }
                 }
             }
@@ -96,7 +96,7 @@ __device__ __forceinline__ void bwd_run(const QkNormParams& p, bool is_q, int ct
     F2 w0[4], w1[4], dw[8], cs[4], sn[4], ns[4];
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[j] = f2(0.f, 0.f);
-    if (NORM) load_gains<DH>(is_q ? p.wq : p.wk, c, w0, w1);
+    if (NORM) load_gains<T, DH>(is_q ? p.wq : p.wk, c, w0, w1);
     const float eps = p.eps;
     auto pos_of = [&](int m) { return m >= N ? 0 : p.pos ? __ldg(p.pos + m) : (int)((unsigned)m % (unsigned)p.T); };
     int pos = ROPE ? pos_of(n) : 0;
@@ -104,7 +104,7 @@ __device__ __forceinline__ void bwd_run(const QkNormParams& p, bool is_q, int ct
 #pragma unroll 1
     for (int item = 0; item < count; ++item) {
         if (ROPE && new_tile) {                         // (its position was fetched with the tile before)
-            lane_angles<T>(pos, s_f, c, cs, sn);
+            lane_angles<T, DH>(pos, s_f, c, cs, sn);
             negate(sn, ns);
             pos = pos_of(n + TOK);
         }
@@ -157,8 +157,8 @@ __device__ __forceinline__ void bwd_run(const QkNormParams& p, bool is_q, int ct
         if (ok) {
             ga.put(g0);
             gb.put(g1);
-            ga.st(out);
-            gb.st(out + HALF);
+            ga.template st<DH>(out);
+            gb.template st<DH>(out + HALF);
         }
         new_tile = ++i == quads;
         if (new_tile) {
@@ -173,9 +173,12 @@ __device__ __forceinline__ void bwd_run(const QkNormParams& p, bool is_q, int ct
     if (!NORM) return;
     __syncthreads();                                    // the queue becomes the rows' sums [row][element]
     float* s_sum = reinterpret_cast<float*>(s_queue);
-    float* mine = s_sum + row * DH + 8 * c;
-    unpairs(dw, mine);
-    unpairs(dw + 4, mine + HALF);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float* mine = s_sum + row * DH + elem_at<T, DH>(c, 2 * j);
+        un2(dw[j], mine[0], mine[1]);
+        un2(dw[4 + j], mine[HALF], mine[HALF + 1]);
+    }
     __syncthreads();
     if (tid < DH) {
         float s = 0.f;

@@ -35,13 +35,6 @@ __device__ __forceinline__ float hsum(F2 a) {
     return x + y;
 }
 // 8 floats as 4 pairs
-__device__ __forceinline__ void pairs16(const float* x, F2* p) {   // x 16-byte aligned
-    const float4 a = reinterpret_cast<const float4*>(x)[0], b = reinterpret_cast<const float4*>(x)[1];
-    p[0] = f2(a.x, a.y);
-    p[1] = f2(a.z, a.w);
-    p[2] = f2(b.x, b.y);
-    p[3] = f2(b.z, b.w);
-}
 __device__ __forceinline__ void pairs(const float* x, F2* p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = f2(x[2 * i], x[2 * i + 1]);
@@ -51,18 +44,20 @@ __device__ __forceinline__ void unpairs(const F2* p, float* x) {
     for (int i = 0; i < 4; ++i) un2(p[i], x[2 * i], x[2 * i + 1]);
 }
 
+// A head's row is spread over CH = DH/16 consecutive lanes; lane c holds 8 elements of the first half and
+// their rotation partners DH/2 further: the 16-byte pieces c (bf16), or c and c + CH (f32) of
+// each half, so that neighbouring lanes always touch neighbouring pieces (f32 rows as 8 contiguous
+// elements a lane cost half of every 32-byte sector: 1B backward 38 us).
+template <typename T, int DH> constexpr int kPieceStep = Vec16<T>::N * (DH / 16);      // elements from a lane's piece to its next
+template <typename T> __device__ __forceinline__ int lane_at(int c) { return Vec16<T>::N * c; }   // its first element
+template <typename T, int DH> __device__ __forceinline__ int elem_at(int c, int e) {              // its e-th
+    return lane_at<T>(c) + e / Vec16<T>::N * kPieceStep<T, DH> + e % Vec16<T>::N;
+}
+
 // 8 activations as loaded: one 16-byte vector (bf16) or two (f32).
 template <typename T> struct Raw8 {
     static constexpr int NV = sizeof(T) / 2;
     uint4 u[NV];
-    __device__ __forceinline__ void ld(const T* p) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) u[i] = make_uint4(0, 0, 0, 0);
-    }
     __device__ __forceinline__ void get(float* x) const {
 #pragma unroll
         for (int i = 0; i < NV; ++i) Vec16<T>::unpack(u[i], x + i * Vec16<T>::N);
@@ -120,11 +115,21 @@ template <typename T> struct Raw8 {
         asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
         return r;
     }
-    __device__ __forceinline__ void st(T* p) const {
+    template <int DH> __device__ __forceinline__ void st(T* p) const {   // p: the lane's first piece
 #pragma unroll
-        for (int i = 0; i < NV; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
+        for (int i = 0; i < NV; ++i) *reinterpret_cast<uint4*>(p + i * kPieceStep<T, DH>) = u[i];
     }
 };
+
+// A lane's 8 of a half row of floats in shared memory (16-byte aligned)
+template <typename T, int DH> __device__ __forceinline__ void pairs_at(const float* x, int c, F2* p) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 a = *reinterpret_cast<const float4*>(x + elem_at<T, DH>(c, 4 * i));
+        p[2 * i] = f2(a.x, a.y);
+        p[2 * i + 1] = f2(a.z, a.w);
+    }
+}
 
 // cos / sin of pos * f, given gt = f / (2 pi): the angle in turns is formed in double precision and its
 // nearest integer removed exactly, so far positions keep the accuracy of the sine of the remainder.
@@ -140,8 +145,7 @@ template <typename T> __device__ __forceinline__ void rope_cs_turn(int pos, doub
     }
 }
 
-// Rows are spread over a CTA as CH = DH/16 consecutive lanes a head, each lane with elements
-// 8c .. 8c+7 and their rotation partners d/2 + 8c ...; every lane of the warp calls.
+// Sum over a row's lanes; every lane of the warp calls.
 template <int CH> __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
     for (int o = CH / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -223,26 +227,27 @@ __device__ __forceinline__ void tile_angles(float* s_cos, float* s_sin, int n0, 
     }
     __syncthreads();
     const int c = tid % (DH / 16), tk = tid / (DH / 16) / kNormHeads;
-    pairs16(s_cos + tk * HALF + 8 * c, cs);
-    pairs16(s_sin + tk * HALF + 8 * c, sn);
+    pairs_at<T, DH>(s_cos + tk * HALF, c, cs);
+    pairs_at<T, DH>(s_sin + tk * HALF, c, sn);
 }
 // A thread's own 8 angles at position pos; s_f: f / (2 pi) of the DH/2 pairs.
-template <typename T> __device__ __forceinline__ void lane_angles(int pos, const double* s_f, int c, F2* cs, F2* sn) {
+template <typename T, int DH> __device__ __forceinline__ void lane_angles(int pos, const double* s_f, int c, F2* cs, F2* sn) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float ca, sa, cb, sb;
-        rope_cs_turn<T>(pos, s_f[8 * c + 2 * i], &ca, &sa);
-        rope_cs_turn<T>(pos, s_f[8 * c + 2 * i + 1], &cb, &sb);
+        rope_cs_turn<T>(pos, s_f[elem_at<T, DH>(c, 2 * i)], &ca, &sa);
+        rope_cs_turn<T>(pos, s_f[elem_at<T, DH>(c, 2 * i + 1)], &cb, &sb);
         cs[i] = f2(ca, cb);
         sn[i] = f2(sa, sb);
     }
 }
 // 8 gains of each half
-template <int DH> __device__ __forceinline__ void load_gains(const float* w, int c, F2* w0, F2* w1) {
+template <typename T, int DH> __device__ __forceinline__ void load_gains(const float* w, int c, F2* w0, F2* w1) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        w0[i] = f2(__ldg(w + 8 * c + 2 * i), __ldg(w + 8 * c + 2 * i + 1));
-        w1[i] = f2(__ldg(w + DH / 2 + 8 * c + 2 * i), __ldg(w + DH / 2 + 8 * c + 2 * i + 1));
+        const float* a = w + elem_at<T, DH>(c, 2 * i);
+        w0[i] = f2(__ldg(a), __ldg(a + 1));
+        w1[i] = f2(__ldg(a + DH / 2), __ldg(a + DH / 2 + 1));
     }
 }
 
@@ -265,12 +270,12 @@ template <typename T, int DH, int NTH> struct NormTile {
                 const int h = (is_q ? i : i - nq4) * kNormHeads + hp;
                 const bool ok = n < N && h < (is_q ? p.H : p.Hkv);
                 const T* x = is_q ? static_cast<const T*>(p.q) : static_cast<const T*>(p.k);
-                const T* s = x + (long long)n * (is_q ? p.q_ld : p.k_ld) + h * DH + 8 * c;
+                const T* s = x + (long long)n * (is_q ? p.q_ld : p.k_ld) + h * DH + lane_at<T>(c);
                 if (ok) {
 #pragma unroll
                     for (int v = 0; v < NV; ++v) {
-                        queue.put(stage, v, s + v * Vec16<T>::N);
-                        queue.put(stage, NV + v, s + HALF + v * Vec16<T>::N);
+                        queue.put(stage, v, s + v * kPieceStep<T, DH>);
+                        queue.put(stage, NV + v, s + HALF + v * kPieceStep<T, DH>);
                     }
                 }
             }
@@ -288,7 +293,7 @@ template <typename T, int DH, int NTH> struct NormTile {
             const bool is_q = i < nq4;
             const float* w = is_q ? p.wq : p.wk;
             if (w != nullptr && w != have) {
-                load_gains<DH>(w, c, w0, w1);
+                load_gains<T, DH>(w, c, w0, w1);
                 have = w;
             }
             fetch(i + (DEPTH - 1) * ny, (stage + DEPTH - 1) % DEPTH);
@@ -307,12 +312,12 @@ template <typename T, int DH, int NTH> struct NormTile {
             if (p.rope) rotate_row(x0, x1, cs, sn, ns);
             const int h = (is_q ? i : i - nq4) * kNormHeads + hp;
             if (n < N && h < (is_q ? p.H : p.Hkv)) {
-                T* d = is_q ? static_cast<T*>(p.q_out) + ((long long)n * p.H + h) * DH + 8 * c
-                            : static_cast<T*>(p.k_out) + ((long long)n * p.Hkv + h) * DH + 8 * c;
+                T* d = is_q ? static_cast<T*>(p.q_out) + ((long long)n * p.H + h) * DH + lane_at<T>(c)
+                            : static_cast<T*>(p.k_out) + ((long long)n * p.Hkv + h) * DH + lane_at<T>(c);
                 a.put(x0);
                 b.put(x1);
-                a.st(d);
-                b.st(d + HALF);
+                a.template st<DH>(d);
+                b.template st<DH>(d + HALF);
             }
         }
         queue.template wait<0>();
