@@ -422,7 +422,8 @@ ua_status ua_qk_norm_rope_bwd(const ua_qk_shape* shape, const void* q, const voi
  * where they are used: one outside [0, pool_pages) raises UA_ERR_INVALID_ARG in the device status and its
  * access is skipped.  capacity < 2^30.
  * A key or value that is not finite makes its whole block's scale NaN when the block is encoded:
- * every output row that sees a slot of that block is then NaN, and no other. */
+ * every output row that sees a slot of that block is then NaN, and no other.  Codes are always
+ * finite (a cache filled by other means must hold finite codes too). */
 typedef enum { UA_KVQ_INT8 = 0, UA_KVQ_E4M3 = 1 } ua_kvq_format;
 
 typedef struct {
@@ -447,7 +448,7 @@ typedef struct {
  * slot's number); values are stored as they are.  q != NULL: queries [B,T,H,d] are normalised and
  * rotated likewise into q_out (all T rows, whatever n_new).  k, v [B,T,Hkv,d] act.
  * start below n_kept takes tokens back (rejected drafts): it must lie on a block's first slot,
- * or its block's earlier rows must still be in the ring: ring_state[b] <= 64*floor(start/64) + 128
+ * or its block's earlier rows must be in the ring: start <= ring_state[b] <= 64*floor(start/64) + 128
  * (always so for up to 64 tokens taken back from the highest slot count).  A start above n_kept, below 0 or without its rows, or n_new
  * outside [0, T], raises UA_ERR_INVALID_ARG in the device status, a sequence that would pass the
  * capacity UA_ERR_CAPACITY; that sequence is left as it was.  Calls on one cache must not overlap on the GPU. */

@@ -30,7 +30,8 @@ __device__ __forceinline__ SeqState seq_state(const KvqAppendParams& p, int b) {
     s.refused = 0;
     if (n0 < 0 || n0 > p.c.cap || s.n_new < 0 || s.n_new > p.n.T || s.start < 0 || s.start > n0)
         s.refused = UA_ERR_INVALID_ARG;
-    else if (s.start % kKvqBlock != 0 && p.c.ring_state[b] > s.start / kKvqBlock * kKvqBlock + kKvqRing)
+    else if (s.start % kKvqBlock != 0 &&
+             (p.c.ring_state[b] < s.start || p.c.ring_state[b] > s.start / kKvqBlock * kKvqBlock + kKvqRing))
         s.refused = UA_ERR_INVALID_ARG;
     else if (s.n_new > p.c.cap - s.start)
         s.refused = UA_ERR_CAPACITY;

@@ -19,7 +19,7 @@ using namespace ua;
 
 namespace {
 
-constexpr int kVersion = 100;   // 0.1.0
+constexpr int kVersion = 200;   // 0.2.0
 constexpr int kBq = 64;         // query tile height of the SIMT attention path
 constexpr int kAppendCtas = 111;        // CTAs an append should have (3/4 of the SMs) before heads share one
 constexpr int kMaxCapacity = 1 << 20;   // decode keeps a capacity/32-word bitmap in shared memory

@@ -220,6 +220,40 @@ def test_refused_sequences_stay_as_they_were(what, start, n_new, code):
     assert int(c.ring_state[-1]) == 0
 
 
+def test_rows_that_were_never_there_are_refused():
+    """A slot count set by hand inside a block has no rows in the ring to encode it from; on a block's border none are
+    needed."""
+    c = make(2, 1, 64, 256, E4, BF)
+    k = normal((2, 70, 1, 64), 45, BF)
+    c.n_kept.copy_(i32([70, 64]))
+    ua.kvq_append(c, k, k, theta=0.0)
+    assert ua.get_device_status() == 1
+    assert c.n_kept.tolist() == [70, 134]
+    want, s = encode(k[1, :64, 0], E4)
+    assert torch.equal(c.k[1, 0, 64:128].view(torch.uint8).cpu(), want)
+
+
+@pytest.mark.parametrize("pos_given", [True, False])
+@pytest.mark.parametrize("start_given", [True, False])
+def test_long_prompts_queries(pos_given, start_given):
+    """So many tokens that the queries take their own kernel (or, with positions that are the slot counts this
+    call changes, not): queries, counts and cache as for a short call, and right before the next kernel."""
+    B, T, H, Hkv, d = 2, 1500, 4, 2, 64
+    c = make(B, Hkv, d, 1600, E4, BF)
+    k0 = normal((B, 64, Hkv, d), 46, BF)
+    ua.kvq_append(c, k0, k0, theta=0.0)
+    q, k, v = normal((B, T, H, d), 47, BF), normal((B, T, Hkv, d), 48, BF), normal((B, T, Hkv, d), 49, BF)
+    pos = (64 + torch.arange(T, dtype=torch.int32)).repeat(B, 1)
+    qo = ua.kvq_append(c, k, v, q, pos=pos.cuda() if pos_given else None, start=i32([64, 64]) if start_given else None)
+    total = qo.float().sum() + c.n_kept.sum()            # (a kernel that does not start early)
+    Q, qb = norm_rope(q, None, pos, 1e-6, THETA)
+    within("q", qo, Q, qb, BF)
+    K, kb = norm_rope(k, None, pos, 1e-6, THETA)
+    check(c, torch.cat([d64(k0), K], 1), torch.cat([k0, v], 1), [T + 64] * B, False, torch.cat([torch.zeros(B, 64, Hkv, d), kb], 1))
+    assert torch.isfinite(total)
+    assert ua.get_device_status() == 0
+
+
 def test_bad_page_is_skipped_and_reported():
     B, Hkv, d = 2, 2, 64
     c = make(B, Hkv, d, 256, E4, BF, 128)
