@@ -377,6 +377,7 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
     using A = Att<T, DH, NT, E4M3>;
     static constexpr long long kNone = -1, kTail = -2, kNoPage = -3;
     static constexpr int kWarps = A::kWarps;
+    static_assert(A::NSTG == 1, "begin_k, begin_v");
     static_assert(16 * DH * sizeof(T) <= A::KB, "a warp's rows of the unfinished block fit a block's place");
     const KvqAttendParams& p;
     typename A::Smem& sm;
@@ -455,11 +456,10 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
         bias0 = p.bias ? p.bias + unit * p.c.cap : nullptr;
 #pragma unroll
         for (int i = 0; i <= A::NSTG; ++i) rows[i] = row_of(i);
-#pragma unroll
-        for (int i = 0; i < A::NSTG; ++i) {
-            load_k(rows[i], i, i);
-            load_v(rows[i], i);
-        }
+    }
+    __device__ __forceinline__ void begin_k() { load_k(rows[0], 0, 0); }
+    __device__ __forceinline__ void begin_v() {
+        load_v(rows[0], 0);
         ks = rows[0] >= 0 ? __ldg(p.c.ks + rows[0]) : 0.f;
         vs = rows[0] >= 0 ? __ldg(p.c.vs + rows[0]) : 0.f;
     }
@@ -739,12 +739,14 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
     // All items and units (below 2^31: checked on the host).  Up to 32 sequences: every warp for itself,
     // a sequence a lane.
     const bool few = p.c.B <= 32;
-    int total = 0, units = 0, my_units = 0, my_blocks = 0;
+    int total = 0, units = 0, my_nq = 0, my_n = 0;
     for (int b = few ? lane : tid; b < p.c.B; b += few ? 32 : kThreads) {
-        total += items_of(b, &my_units);
-        units += my_units;
+        counts(b, &my_nq, &my_n);
+        const int u = Hkv * tiles_of(my_nq);
+        total += u * (blocks_of(my_n) + kUnitCost);
+        units += u;
     }
-    if (few && my_units > 0) my_blocks = total / my_units - kUnitCost;
+    const int my_units = units, my_blocks = blocks_of(my_n);     // (few: of this lane's sequence)
     total = __reduce_add_sync(0xffffffffu, total);
     units = __reduce_add_sync(0xffffffffu, units);
     if (!few) {
@@ -847,21 +849,21 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
         const int l = __ffs(past) - 1, k = __shfl_sync(0xffffffffu, parts, l);
         const int off = cta - __shfl_sync(0xffffffffu, inc - my_units * parts, l), u = off / k, part = off - u * k;
         s.b = l;
-        counts(l, &s.nq, &s.n);
+        s.nq = __shfl_sync(0xffffffffu, my_nq, l);
+        s.n = __shfl_sync(0xffffffffu, my_n, l);
         s.nb = blocks_of(s.n);
         const int tiles = tiles_of(s.nq);
-        s.h = u / tiles;
+        s.h = tiles == 1 ? u : u / tiles;
         s.rt = u - s.h * tiles;
-        s.k0 = (int)((long long)part * s.nb / k);
-        s.k1 = (int)((long long)(part + 1) * s.nb / k);
+        s.k0 = (int)((unsigned)part * (unsigned)s.nb / (unsigned)k);         // (at most 148 * 2^24)
+        s.k1 = (int)((unsigned)(part + 1) * (unsigned)s.nb / (unsigned)k);
         s.r_lo = cta - part;
         s.r_hi = s.r_lo + k - 1;
         s.off = s.len = 0;
         return s;
     };
     Walk<T, DH, NT, E4M3> walk(p, sm);
-    // Queries of a tile: 8 threads a row, fetched before the segment's copies are started so that
-    // they need not queue behind them.
+    // Queries of a tile: 8 threads a row, fetched before the segment's copies are started.
     constexpr int E = DH / 8, QV = E / Vec16<T>::N;
     uint4 qraw[QV];
     auto start = [&](const Segment& s) {
@@ -883,6 +885,7 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
     Segment cur = aligned ? own_part(&have) : find();
     if (!have) return;
     start(cur);
+    bool ahead = false;                                  // the segment's keys are on their way
     for (;;) {
         const int h = cur.h, rt = cur.rt, nq = cur.nq, n = cur.n, b = cur.b, r_lo = cur.r_lo, r_hi = cur.r_hi;
         if (tid < 8 * R) {
@@ -933,6 +936,10 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
             }
         }
         __syncthreads();
+        // (An SM takes in 25 bytes a clock and a copy waits for room to be issued: with all copies before
+        // the barrier the first warp's keys lay there for 5000 clocks until the last warp's were issued.)
+        if (!ahead) walk.begin_k();
+        walk.begin_v();
         State<DH, NT> st;
         init_state<DH, NT>(st);
         walk.run(st);
@@ -942,7 +949,11 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
         if (more) {
             cur = segment(b, cur.off + cur.len);
             more = cur.k1 > cur.k0;
-            if (more) start(cur);
+            if (more) {
+                start(cur);
+                walk.begin_k();
+            }
+            ahead = more;
         }
 
         // merge the warps: statistics, then O, one warp after the other
@@ -994,14 +1005,37 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
             }
         }
         const int rows = min(R, nq * G - rt * R);
-        auto put_out = [&](int row, int d4, float4 o, float M, float L) {
-            const int gr = rt * R + row, i = gr / G, head = h * G + gr - i * G;
-            const size_t at = (((size_t)b * p.Tq + i) * p.H + head) * DH + d4;
+        // four elements of a row: where they lie, their gates (fetched ahead of the merge), their output
+        auto place = [&](int row, int d4, int* head, int* i) {
+            const int gr = rt * R + row;
+            *i = gr / G;
+            *head = h * G + gr - *i * G;
+            return (((size_t)b * p.Tq + *i) * p.H + *head) * DH + d4;
+        };
+        auto gates = [&](int row, int d4) {
+            float4 f = make_float4(0, 0, 0, 0);
+            if (p.g) {
+                int head, i;
+                const T* src = static_cast<const T*>(p.g) + place(row, d4, &head, &i);
+                if constexpr (A::F32) {
+                    f = *reinterpret_cast<const float4*>(src);
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(src);
+                    f = make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+                }
+            }
+            return f;
+        };
+        auto put_out = [&](int row, int d4, float4 o, float M, float L, float4 gt) {
+            int head, i;
+            const size_t at = place(row, d4, &head, &i);
             const float inv = L != 0.f ? 1.f / L : 0.f;
             float y[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
             if (p.g) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] *= sigmoid_f(Elem<T>::ld(static_cast<const T*>(p.g) + at + e));
+                y[0] *= sigmoid_f(gt.x);
+                y[1] *= sigmoid_f(gt.y);
+                y[2] *= sigmoid_f(gt.z);
+                y[3] *= sigmoid_f(gt.w);
             }
             T* out = static_cast<T*>(p.o) + at;
             if constexpr (A::F32) {
@@ -1034,7 +1068,7 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
                 o.w += o1.y;
             }
             if (whole) {
-                put_out(row, d4, o, M, L);
+                put_out(row, d4, o, M, L, gates(row, d4));
             } else {
                 __stcg(reinterpret_cast<float4*>(to + 2 * R + row * DH + d4), o);
                 if (d4 == 0) {
@@ -1072,6 +1106,7 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
                     const int grp = groups > 1 ? tid / cols : 0, e = e0 + tid - grp * cols;
                     const int row = e / (DH / 4), d4 = (e % (DH / 4)) * 4;
                     const bool on = e < cols && grp < groups;
+                    const float4 gt = on && grp == 0 ? gates(row, d4) : make_float4(0, 0, 0, 0);
                     float M = -INFINITY, L = 0.f;
                     float4 o = make_float4(0, 0, 0, 0);
                     auto join = [&](float m, float l, float4 v) {
@@ -1112,7 +1147,7 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
                             join(ml.x, ml.y, share_o[g * cols + tid]);
                         }
                     }
-                    if (on && grp == 0) put_out(row, d4, o, M, L);
+                    if (on && grp == 0) put_out(row, d4, o, M, L, gt);
                 }
             }
         }

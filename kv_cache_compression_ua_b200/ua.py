@@ -632,7 +632,7 @@ def _heads(name, t, B, T, d, dtype, dev):
 
 def _like(x):
     """A dense tensor like x (which may be a slice of a larger one)."""
-    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def _addr(t):
