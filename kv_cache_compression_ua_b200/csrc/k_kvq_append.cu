@@ -1,13 +1,16 @@
 // k_kvq_append.cu -- append of keys and values to the 8-bit cache: per-head norm and position
 // rotation of the keys on the way, the ring of recent rows, and the encoding of every block of 64
-// slots that the call fills; the step's queries are normalised and rotated by further CTAs of
-// the same launch (formulas and layout in include/ua.h).
+// slots that the call fills; a step's queries are normalised and rotated by further CTAs of the
+// same launch, a prompt's by k_qk_norm_fwd beside it (formulas and layout in include/ua.h).
 //
 // Bound: HBM for prompts (each key and value read once in the activation type, written once in
 // 8 bits), launch latency for single tokens.  One CTA owns a block of 64 slots of hpc KV heads:
 // CH = DH/16 lanes a row, every element of the block in registers between the one read and the
-// write of its code, so the block's largest magnitude costs one reduction and no second read.
-// The thread's eight angles are formed once and serve all hpc heads.
+// write of its code, so the block's largest magnitude costs one reduction and no second read.  A
+// token's gain and rotation are one set of coefficients for all hpc heads; the next head's rows are
+// copied meanwhile (a thread's own queue).  32 x 4096 tokens, 8 heads of 64, bf16 to e4m3: 83 us,
+// 4.8 TB/s; issue slots bind (its share of a prompt with 32 query heads: half, 8 x 4096 tokens 63 us
+// together, 84 % of the copy bandwidth).  The step of 32 tokens: 5.2 us.
 #include "qk_norm.cuh"
 #include "ua_profile.h"
 

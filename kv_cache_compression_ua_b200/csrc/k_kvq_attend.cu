@@ -4,26 +4,33 @@
 // Bound: HBM, the codes read once: 2 * DH bytes a slot and KV head, 6.5 TB/s / 148 SMs = 23 bytes
 // a clock and SM.  The arithmetic has to hide under that, so nothing is converted twice and no
 // thread does a dot product on the CUDA cores:
-//   * one warp walks blocks of 64 slots with its own asynchronous copies (16 KB of shared memory a
-//     warp, no block barrier in the walk);
-//   * both products run on the tensor cores with the CODES as the 16-row operand and the (at most 16) query rows
-//     as the 8-wide one: S^T = K Q^T and O^T = V^T P^T, so a token with 4 query heads wastes half
-//     of a small product and not three quarters of a large one.  (A tcgen05 tile of 128 rows
-//     would want the probabilities back through shared memory and TMEM for products of 8
-//     columns; mma.sync keeps them in registers, and the products are far from being the bound);
-//   * codes become f16 exactly (int8 and e4m3 both are f16 values), two a conversion; the scale of
-//     a block multiplies its logits (keys) and its 16 partial sums a thread (values) in fp32;
+//   * one warp walks blocks of 64 slots with its own asynchronous copies (a block's keys and values,
+//     8 or 16 KB of shared memory a warp; no block barrier in the walk); one CTA of 16 (DH = 64), 12
+//     (DH = 128) or 8 warps (more than 8 rows) an SM, so that few parts have to be merged;
+//   * both products run on the tensor cores with the CODES as the 16-row operand and the (at most 16)
+//     query rows as the 8-wide one: S^T = K Q^T and O^T = V^T P^T, so a token with 4 query heads wastes
+//     half of a small product and not three quarters of a large one.  (A tcgen05 tile of 128 rows
+//     would want the probabilities back through shared memory and TMEM for products of 8 columns;
+//     mma.sync keeps them in registers, and the tensor pipe is 15 % busy);
+//   * codes become f16 exactly and cheaply: e4m3 by its conversion, int8 as subnormals (codes_f16); the
+//     scale of a block multiplies its logits (keys) and its partial sums (values) in fp32;
 //   * the contraction may run over the head's elements in any order: a lane takes 16 contiguous bytes of
-//     a key as the operand's scattered elements; for the values, four tokens' bytes are
-//     transposed in registers.
+//     a key as the operand's scattered elements; for the values, tokens' bytes are paired in registers;
+//   * a logit is one fused multiply-add and an exp2 from the product where nothing is masked.
 // Queries enter as f16 scaled by a power of two for each row (bf16 queries exactly; fp32 ones as a high
 // and a low part), probabilities as f16 times 2^14 (fp32: high and low part), so that small
 // probabilities of long caches keep 2^-38 of the row's maximum; sums and statistics are fp32.
 //
-// Split: the (sequence, KV head, row tile, block) items of all sequences are laid out flat and cut
-// into equal runs, one for each CTA, whatever the lengths; the lengths are read on the device.  A
-// unit (sequence, head, row tile) that lies in several CTAs' runs is merged by the last of them
-// to arrive, in the order of the runs.
+// Split, by lengths read on the device: few units (sequence, KV head, row tile) get whole CTAs each;
+// otherwise the blocks of all units are laid out flat, with kUnitCost more for each unit, and cut into equal runs,
+// one a CTA.  A unit in several CTAs is merged by the last of them to arrive, in the order of the blocks:
+// the result does not depend on who that is.
+//
+// Measured: 32 sequences of about 16k slots, 8 heads of 64, int8 (448 MB): 80 us, 5.6 TB/s (86 % of the copy bandwidth;
+// the copies alone 74 us; what is left is the ALU pipe, 2 clocks a warp instruction); one of
+// 262144 slots, 8 heads of 128, e4m3 (537 MB): 93 us, 5.8 TB/s (88 %; the copies alone 85 us, SMs of the
+// larger clusters finish last); 4 of about 8192 with bias and gate (57 MB): 22 us, of it 7 us before the
+// first products and 5 us of merging; one of 333 slots: 7.4 us.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -764,7 +771,7 @@ __global__ void __launch_bounds__(Att<T, DH, NT, E4M3>::kThreads, 1) k_kvq_atten
     }
     const int cta = blockIdx.x, grid = gridDim.x;
     // Few units: whole CTAs for each, `run` blocks each at most -- a CTA with parts of two units would
-    // pay for starting and merging twice (3B decode with bias: 29 us; 21 us so).
+    // pay for starting and merging twice (3B decode with bias: 29 us; 22 us so).
     const bool aligned = few && units * 2 <= grid;
     // Otherwise equal runs of items, one a CTA.
     const int ctas = max(min(units, grid), min(grid, (total + A::kMinItems - 1) / A::kMinItems));
