@@ -446,7 +446,8 @@ typedef struct {
  * .. (start [B] int32 or NULL: n_kept[b]), then n_kept[b] = start[b] + n_new[b].  Keys are normalised (wk
  * != NULL) and rotated as in ua_qk_norm_rope_fwd on the way, with pos [B,T] int32 or NULL (the
  * slot's number); values are stored as they are.  q != NULL: queries [B,T,H,d] are normalised and
- * rotated likewise into q_out (all T rows, whatever n_new).  k, v [B,T,Hkv,d] act.
+ * rotated likewise into q_out (all T rows, whatever n_new).  k, v [B,T,Hkv,d] act.  start, and a
+ * single token's pos, may be n_kept itself.
  * start below n_kept takes tokens back (rejected drafts): it must lie on a block's first slot,
  * or its block's earlier rows must be in the ring: start <= ring_state[b] <= 64*floor(start/64) + 128
  * (always so for up to 64 tokens taken back from the highest slot count).  A start above n_kept, below 0 or without its rows, or n_new
@@ -466,8 +467,10 @@ ua_status ua_kvq_append(const ua_kvq* cache, const ua_qk_shape* shape, const voi
  * sees nothing gets o = 0, lse = -inf; rows i >= n_q[b] of o and lse are left as they were.
  * Any Tq >= 1; made for single tokens and drafts (16 rows Tq*H/Hkv per pass over the cache).
  * n_kept outside [0, capacity] or n_q outside [0, Tq] raises UA_ERR_INVALID_ARG in the device
- * status and the sequence is taken as empty.  ws: as for ua_decode_step_split, zeroed once before its first use;
- * its counters are zero again after every call; calls that share it must not overlap on the GPU. */
+ * status and the sequence is taken as empty.  ws: zeroed once before its first use (and again after
+ * using it for anything else); its counters are zero again after every call, so calls of any shapes
+ * may share it (of the largest size among them), one after another: they must not overlap on the GPU.  A
+ * counter that is found too high raises UA_ERR_INVALID_ARG in the device status. */
 ua_status ua_kvq_attend_workspace_size(const ua_kvq* cache, int H, int Tq, size_t* bytes);
 ua_status ua_kvq_attend(const ua_kvq* cache, int H, int Tq, const void* q, const void* g, const float* bias,
                         const int32_t* n_q, float scale, void* o, float* lse, void* ws, size_t ws_bytes,

@@ -152,10 +152,13 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
         const SeqState s = seq_state(p, b);
         if (s.refused && j == 0 && gi == 0 && tid == 0) raise_status(s.refused);
         if (tid < HALF) s_f[tid] = p.n.rf.f[tid] * 0.15915494309189535;      // 1 / (2 pi)
-        __syncthreads();
-        arrive();
         const int end = s.start + s.n_new, j0 = s.start / kKvqBlock, jl = end / kKvqBlock;   // jl: unfinished block
         const int mine = j0 + j;
+        // this row's position (a single token's may be the slot count: read before anyone changes it)
+        const int t_mine = mine * kKvqBlock + row - s.start;
+        const int pos_mine = p.n.rope && p.n.pos && t_mine >= 0 && t_mine < s.n_new ? p.n.pos[b * T_ + t_mine] : 0;
+        __syncthreads();
+        arrive();
         if (s.n_new > 0 && mine * kKvqBlock < end) {
             // Ring rows are kept for blocks jl - 1 and jl.  The first block may still need earlier
             // rows out of the ring, from the places that the kept block of the same parity takes:
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
                 F2 c00[4], c01[4], c11[4], c10[4];
                 if (is_new && p.n.rope) {
                     F2 cs[4], sn[4];
-                    lane_angles<T, DH>(p.n.pos ? p.n.pos[n] : slot, s_f, c, cs, sn);
+                    lane_angles<T, DH>(!p.n.pos ? slot : pass == 0 ? pos_mine : p.n.pos[n], s_f, c, cs, sn);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         c00[i] = c11[i] = cs[i];

@@ -278,13 +278,13 @@ int kvq_row_tiles(const ua_kvq* c, int H, int Tq) {
     return (rows + R - 1) / R;
 }
 
-size_t kvq_ws_counters(const ua_kvq* c, int H, int Tq) {
-    return round_up((size_t)c->B * c->Hkv * kvq_row_tiles(c, H, Tq) * 4, 256);
-}
+// The runs' parts of the largest row tile, whatever the shape, then the counters: so calls of any shapes
+// find zeros where they count (2.5 MB).
+constexpr size_t kKvqPartBytes = (size_t)kKvqAttendCtas * 2 * 16 * (128 + 2) * 4;
+static_assert(kKvqPartBytes % 256 == 0, "aligned counters");
 
 size_t kvq_ws_bytes(const ua_kvq* c, int H, int Tq) {
-    const int R = kvq_row_tile(Tq * (H / c->Hkv));
-    return kvq_ws_counters(c, H, Tq) + (size_t)kKvqAttendCtas * 2 * R * (c->d + 2) * 4;
+    return kKvqPartBytes + round_up((size_t)c->B * c->Hkv * kvq_row_tiles(c, H, Tq) * 4, 256);
 }
 
 ua_status check_kvq_heads(const ua_kvq* c, int H, int Tq) {
@@ -1021,8 +1021,9 @@ ua_status ua_kvq_append(const ua_kvq* c, const ua_qk_shape* s, const void* q, co
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     // The queries of many tokens run in their own kernel beside the blocks' one (smaller CTAs, more of
     // them an SM); those of a few steps in further CTAs of the same launch, as do queries whose positions
-    // are slot counts that this call changes.
-    const bool apart = q && p.n.N >= 148 * 16 && (pos || start || !p.n.rope);
+    // are slot counts that this call changes (given as start or pos, too: those CTAs read them first).
+    const bool apart = q && p.n.N >= 148 * 16 &&
+                       (!p.n.rope || (pos ? pos != c->n_kept : start != nullptr && start != c->n_kept));
     if (q && !apart) {
         p.q_tiles = (int)((p.n.N + 15) / 16);
         const int quads = (s->H + 3) / 4;
@@ -1068,8 +1069,8 @@ ua_status ua_kvq_attend(const ua_kvq* c, int H, int Tq, const void* q, const voi
     p.c = kvq_view(c);
     p.H = H; p.G = H / c->Hkv; p.Tq = Tq; p.RT = kvq_row_tiles(c, H, Tq);
     p.scale = scale; p.q = q; p.g = g; p.bias = bias; p.n_q = n_q; p.o = o; p.lse = lse;
-    p.cnt = static_cast<unsigned*>(ws);
-    p.part = reinterpret_cast<float*>(at(ws, kvq_ws_counters(c, H, Tq)));
+    p.part = static_cast<float*>(ws);
+    p.cnt = reinterpret_cast<unsigned*>(at(ws, kKvqPartBytes));
     return cuda_status(launch_kvq_attend(p, c->d, c->dtype == UA_BF16, c->format == UA_KVQ_E4M3,
                                          static_cast<cudaStream_t>(stream)));
 }

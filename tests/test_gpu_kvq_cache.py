@@ -254,6 +254,24 @@ def test_long_prompts_queries(pos_given, start_given):
     assert ua.get_device_status() == 0
 
 
+@pytest.mark.parametrize("B,T,what", [(2, 3000, "start"), (3, 1, "pos"), (2600, 1, "pos"), (2600, 1, "start")])
+def test_slot_counts_themselves_as_positions(B, T, what):
+    """n_kept given as start or as a token's position: what the call found there, though it changes it."""
+    H, Hkv, d = 4, 2, 64
+    a, e = make(B, Hkv, d, T + 128, E4, BF), make(B, Hkv, d, T + 128, E4, BF)
+    k0, n0 = normal((B, 70, Hkv, d), 91, BF), i32([i % 71 for i in range(B)])
+    q, k, v = normal((B, T, H, d), 92, BF), normal((B, T, Hkv, d), 93, BF), normal((B, T, Hkv, d), 94, BF)
+    for c in (a, e):
+        ua.kvq_append(c, k0, k0, n_new=n0, theta=0.0)
+    of = lambda x: x if what == "start" else x[:, None]  # noqa: E731
+    got = ua.kvq_append(a, k, v, q, **{what: of(a.n_kept)})
+    want = ua.kvq_append(e, k, v, q, **{what: of(n0)})
+    assert torch.equal(got, want)
+    for name in ("k", "v", "k_scale", "v_scale", "k_ring", "v_ring", "ring_state", "n_kept"):
+        assert same_bits(getattr(a, name), getattr(e, name)), name
+    assert ua.get_device_status() == 0
+
+
 def test_bad_page_is_skipped_and_reported():
     B, Hkv, d = 2, 2, 64
     c = make(B, Hkv, d, 256, E4, BF, 128)
