@@ -11,7 +11,7 @@
 //     query rows as the 8-wide one: S^T = K Q^T and O^T = V^T P^T, so a token with 4 query heads wastes
 //     half of a small product and not three quarters of a large one.  (A tcgen05 tile of 128 rows
 //     would want the probabilities back through shared memory and TMEM for products of 8 columns;
-//     mma.sync keeps them in registers, and the tensor pipe is 15 % busy);
+//     mma.sync keeps them in registers, and the tensor pipe is 20 % busy);
 //   * codes become f16 exactly and cheaply: e4m3 by its conversion, int8 as subnormals (codes_f16); the
 //     scale of a block multiplies its logits (keys) and its partial sums (values) in fp32;
 //   * the contraction may run over the head's elements in any order: a lane takes 16 contiguous bytes of

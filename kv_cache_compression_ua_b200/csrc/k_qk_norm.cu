@@ -8,7 +8,7 @@
 //   * few instructions an element, for at 6.5 TB/s an SM has some 280 issue slots a warp for 3 KB: packed
 //     fp32 arithmetic, a token's angles once for all its heads (90 -> 83 us; copy bandwidth: 82);
 //   * the backward's angles a thread's own, without barriers, from positions fetched a tile ahead: 169 ->
-//     140 us (123), 88 % of the copy bandwidth; what is left is issue slots (52 % busy at 16 warps an SM,
+//     140 us (123), 88 % of the copy bandwidth; what is left is issue slots (58 % busy at 16 warps an SM,
 //     128 registers a thread).
 #include "qk_norm.cuh"
 #include "ua_profile.h"
@@ -238,9 +238,10 @@ int head_quads(const QkNormParams& p) {
 template <typename T, int DH> cudaError_t fwd(const QkNormParams& p, cudaStream_t s) {
     constexpr int TOK = norm_tokens<DH, kNth>(), smem = NormTile<T, DH, kNth>::Queue::kBytes;
     const long long tiles = (p.N + TOK - 1) / TOK;
-    // few tokens: the heads are split over CTAs too, until there is about one for each SM
-    const int quads = head_quads(p);
-    const int split = (int)(tiles >= 148 ? 1 : (quads < 148 / tiles ? quads : 148 / tiles));
+    // few tokens: the heads are split over CTAs too, while all of them fit the SMs' three places (2 x 777
+    // tokens, 32 + 8 heads of 64: 7.1 us with a CTA an SM, 5.2 with three; in two rounds, 6.2)
+    const int quads = head_quads(p), places = 3 * 148;
+    const int split = (int)(tiles >= places ? 1 : (quads < places / tiles ? quads : places / tiles));
     cudaError_t e = cudaFuncSetAttribute(k_qk_norm_fwd<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     UA_PROFILE("k_qk_norm_fwd", s);
