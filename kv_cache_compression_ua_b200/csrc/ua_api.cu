@@ -1012,10 +1012,18 @@ ua_status ua_kvq_append(const ua_kvq* c, const ua_qk_shape* s, const void* q, co
     // idle (3B chunk of 4 x 1003 tokens: one head each 30 us, two 22 us).  A step of less than a block
     // has a row or a few a CTA and is latency: one head each (32 tokens of the 1B shape, cold: 7.3 us, two
     // heads 9.4 us).
+    // More CTAs also where they cut the rounds that the SMs' places take, each as long as its heads, by a
+    // fifth (1B shape, with queries: 8 x 4096 tokens, 520 CTAs of 8 heads 72.4 us, 1040 of four 68.8; 12 x 4096,
+    // rounds alike, 97.5 and 98.0); below four heads the repeated angles cost as much (4 x 1003 tokens, four
+    // heads 11.9, two 13.7).
     p.hpc = s->T < kKvqBlock ? 1 : s->Hkv;
-    while (p.hpc > 1 && (long long)s->B * p.nb * (s->Hkv / p.hpc) < kAppendCtas) {
+    const int places = s->d == 64 ? 3 * 148 : 148;
+    auto ctas = [&](int hpc) { return (long long)s->B * p.nb * (s->Hkv / hpc); };
+    auto length = [&](int hpc) { return (ctas(hpc) + places - 1) / places * hpc; };
+    while (p.hpc > 1) {
         int next = p.hpc - 1;
         while (s->Hkv % next) --next;
+        if (ctas(p.hpc) >= kAppendCtas && (next < 4 || 5 * length(next) > 4 * length(p.hpc))) break;
         p.hpc = next;
     }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
