@@ -643,10 +643,16 @@ def _addr(t):
 _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _raw_stream(stream, dev):
-    if stream is None and _current_raw is not None:
-        return _current_raw(dev.index)
-    return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+def _raw_stream(dev):
+    return _current_raw(dev.index) if _current_raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _on_stream(stream, like, fn, *args, **kw):
+    """fn with `stream` current: outputs and scratch (zeroed there) then belong to the stream they are used on."""
+    if like is not None and stream.device != like.device:
+        raise ValueError(f"stream: on {stream.device}, the call runs on {like.device}")
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
 
 
 def _launch(name, dev, fn, *args):
@@ -701,6 +707,9 @@ def qk_norm_rope_fwd(q, k, wq=None, wk=None, *, pos=None, eps=1e-6, theta=500000
     """ua_qk_norm_rope_fwd: RMS norm of every head with the gains wq, wk [d] (None: no norm on that
     side) and the position rotation (theta 0: none), q [B,T,H,d] and k [B,T,Hkv,d] in one pass.  Either may
     be None; both may be slices of a fused projection's output.  Returns dict(q, k)."""
+    if stream is not None:
+        return _on_stream(stream, k if q is None else q, qk_norm_rope_fwd, q, k, wq, wk, pos=pos, eps=eps, theta=theta,
+                          q_out=q_out, k_out=k_out)
     shape, dev, dt = _qk_shape(q, k, wq, wk, pos, eps, theta)
     for name, x, y in (("q_out", q, q_out), ("k_out", k, k_out)):
         if y is not None:
@@ -712,7 +721,7 @@ def qk_norm_rope_fwd(q, k, wq=None, wk=None, *, pos=None, eps=1e-6, theta=500000
     if k is not None and k_out is None:
         k_out = _like(k)
     _launch("ua_qk_norm_rope_fwd", dev, load_library().ua_qk_norm_rope_fwd, ctypes.byref(shape), _addr(q), _addr(k),
-            _addr(wq), _addr(wk), _addr(pos), _addr(q_out), _addr(k_out), _raw_stream(stream, dev))
+            _addr(wq), _addr(wk), _addr(pos), _addr(q_out), _addr(k_out), _raw_stream(dev))
     return {"q": q_out, "k": k_out}
 
 
@@ -726,6 +735,9 @@ def qk_norm_rope_bwd_workspace_size(shape: ua_qk_shape) -> int:
 def qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, *, pos=None, eps=1e-6, theta=500000.0, ws=None, stream=None):
     """ua_qk_norm_rope_bwd: gradients of the forward with the same arguments.  Returns dict(dq, dk,
     dwq, dwk), None for what the forward did not have."""
+    if stream is not None:
+        return _on_stream(stream, k if q is None else q, qk_norm_rope_bwd, q, k, wq, wk, dq_out, dk_out, pos=pos, eps=eps,
+                          theta=theta, ws=ws)
     shape, dev, dt = _qk_shape(q, k, wq, wk, pos, eps, theta)
     for name, x, y in (("dq_out", q, dq_out), ("dk_out", k, dk_out)):
         if (x is None) != (y is None):
@@ -743,7 +755,7 @@ def qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, *, pos=None, eps=1e-6, theta=
     dwk = None if k is None or wk is None else torch.empty_like(wk)
     _launch("ua_qk_norm_rope_bwd", dev, load_library().ua_qk_norm_rope_bwd, ctypes.byref(shape), _addr(q), _addr(k),
             _addr(wq), _addr(wk), _addr(pos), _addr(dq_out), _addr(dk_out), _addr(dq), _addr(dk), _addr(dwq),
-            _addr(dwk), ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
+            _addr(dwk), ws.data_ptr(), _nbytes(ws), _raw_stream(dev))
     return {"dq": dq, "dk": dk, "dwq": dwq, "dwk": dwk}
 
 
@@ -848,6 +860,9 @@ def kvq_append(cache: KVQCache, k, v, q=None, *, wq=None, wk=None, pos=None, n_n
     """ua_kvq_append: append k, v [B,T,Hkv,d] (the first n_new[b] tokens of sequence b), the keys
     normalised (wk) and rotated on the way; start [B] int32 takes tokens back first.  With q [B,T,H,d]
     the queries are normalised (wq) and rotated in the same launch and returned."""
+    if stream is not None:
+        return _on_stream(stream, cache, kvq_append, cache, k, v, q, wq=wq, wk=wk, pos=pos, n_new=n_new, start=start,
+                          eps=eps, theta=theta, q_out=q_out)
     if k is None or v is None:
         raise ValueError("k and v are needed")
     shape, dev, dt = _qk_shape(q, k, wq, wk, pos, eps, theta, v)
@@ -868,7 +883,7 @@ def kvq_append(cache: KVQCache, k, v, q=None, *, wq=None, wk=None, pos=None, n_n
         _dense("q_out", q_out, q.shape, (dt,), dev)
     _launch("ua_kvq_append", dev, load_library().ua_kvq_append, cache._ref, ctypes.byref(shape), _addr(q), k.data_ptr(),
             v.data_ptr(), _addr(wq), _addr(wk), _addr(pos), _addr(n_new), _addr(start), _addr(q_out),
-            _raw_stream(stream, dev))
+            _raw_stream(dev))
     return q_out
 
 
@@ -886,6 +901,8 @@ def kvq_attend(cache: KVQCache, q, *, g=None, bias=None, n_q=None, scale=None, o
     them) over the cache.  bias [B,Hkv,capacity] f32 is added to the logits, g (like q) gates the output, lse
     [B,H,Tq] f32 receives the row normalisers.  ws: kvq_attend_workspace_size bytes, zeroed once (a fresh
     one is made without it).  Returns o, shaped like q."""
+    if stream is not None:
+        return _on_stream(stream, cache, kvq_attend, cache, q, g=g, bias=bias, n_q=n_q, scale=scale, out=out, lse=lse, ws=ws)
     if q.dim() not in (3, 4):
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [B, H, d] or [B, Tq, H, d]")
     dev, dt, qs = cache.device, cache.dtype, q.shape
@@ -912,7 +929,7 @@ def kvq_attend(cache: KVQCache, q, *, g=None, bias=None, n_q=None, scale=None, o
         raise ValueError("ws: a contiguous tensor on the call's device is needed")
     _launch("ua_kvq_attend", dev, load_library().ua_kvq_attend, cache._ref, H, Tq, q.data_ptr(), _addr(g), _addr(bias),
             _addr(n_q), float(d) ** -0.5 if scale is None else float(scale), out.data_ptr(), _addr(lse), ws.data_ptr(),
-            _nbytes(ws), _raw_stream(stream, dev))
+            _nbytes(ws), _raw_stream(dev))
     return out
 
 

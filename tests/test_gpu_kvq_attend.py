@@ -283,8 +283,38 @@ def test_on_another_stream_and_as_three_dimensional_queries():
     c = filled(2, 2, 64, [300, 70], E4, BF, seed=51)
     q = normal((2, 8, 64), 52, BF)
     want = ua.kvq_attend(c, q[:, None].contiguous())[:, 0]
+    ws = ua.alloc_workspace(ua.kvq_attend_workspace_size(c, 8), "cuda")
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
-    o = ua.kvq_attend(c, q, stream=s, ws=ua.alloc_workspace(ua.kvq_attend_workspace_size(c, 8), "cuda"))
+    o = ua.kvq_attend(c, q, stream=s, ws=ws)
     s.synchronize()
     assert o.shape == q.shape and torch.equal(o, want)
+
+
+def test_a_layer_on_a_stream_of_its_own():
+    """Every call with stream=, outputs and scratch made by the wrappers, while the current stream is busy (and its
+    free memory is full of ones): nothing of the calls is queued there."""
+    B, T, H, Hkv, d = 2, 900, 8, 2, 64
+    q, k, v = normal((B, T, H, d), 41, BF), normal((B, T, Hkv, d), 42, BF), normal((B, T, Hkv, d), 43, BF)
+    wq, wk = 1 + 0.2 * normal((d,), 44, F), 1 + 0.2 * normal((d,), 45, F)
+    last = q[:, -1:].contiguous()
+
+    def layer(c, **kw):
+        qo = ua.kvq_append(c, k, v, q, wq=wq, wk=wk, **kw)
+        o = ua.kvq_attend(c, last, **kw)
+        f = ua.qk_norm_rope_fwd(q, k, wq, wk, **kw)
+        g = ua.qk_norm_rope_bwd(q, k, wq, wk, q, k, **kw)
+        return [qo, o, *f.values(), *g.values()]
+
+    a, b = make(B, Hkv, d, 1024, E4, BF), make(B, Hkv, d, 1024, E4, BF)
+    want = layer(a)
+    s = torch.cuda.Stream()
+    junk = [torch.full((n,), 0x7f, dtype=torch.uint8, device="cuda") for n in (1 << 16, 1 << 20, 3 << 20, 1 << 22)]
+    torch.cuda.synchronize()
+    del junk
+    torch.cuda._sleep(100_000_000)
+    got = layer(b, stream=s)
+    s.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    assert ua.get_device_status() == 0
