@@ -449,7 +449,7 @@ typedef struct {
  * rotated likewise into q_out (all T rows, whatever n_new).  k, v [B,T,Hkv,d] act.  start, and a
  * single token's pos, may be n_kept itself.
  * start below n_kept takes tokens back (rejected drafts): it must lie on a block's first slot,
- * or its block's earlier rows must be in the ring: start <= ring_state[b] <= 64*floor(start/64) + 128
+ * or its block's earlier rows must be in the ring: start <= ring_state[b] < 64*floor(start/64) + 128
  * (always so for up to 64 tokens taken back from the highest slot count).  A start above n_kept, below 0 or without its rows, or n_new
  * outside [0, T], raises UA_ERR_INVALID_ARG in the device status, a sequence that would pass the
  * capacity UA_ERR_CAPACITY; that sequence is left as it was.  Calls on one cache must not overlap on the GPU. */

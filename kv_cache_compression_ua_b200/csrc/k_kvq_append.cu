@@ -24,7 +24,8 @@ struct SeqState {
 };
 
 // What sequence b appends.  Refused: n_new or start out of range, earlier rows of the start's
-// block no longer in the ring, capacity.
+// block not in the ring, capacity.  A call that ends with `end` slots keeps the rows of blocks end/64 - 1 and
+// end/64 (at a border the latter has none yet), so only those of the highest count are sure to be there.
 __device__ __forceinline__ SeqState seq_state(const KvqAppendParams& p, int b) {
     SeqState s;
     const int n0 = p.c.n_kept[b];
@@ -34,7 +35,7 @@ __device__ __forceinline__ SeqState seq_state(const KvqAppendParams& p, int b) {
     if (n0 < 0 || n0 > p.c.cap || s.n_new < 0 || s.n_new > p.n.T || s.start < 0 || s.start > n0)
         s.refused = UA_ERR_INVALID_ARG;
     else if (s.start % kKvqBlock != 0 &&
-             (p.c.ring_state[b] < s.start || p.c.ring_state[b] > s.start / kKvqBlock * kKvqBlock + kKvqRing))
+             (p.c.ring_state[b] < s.start || s.start / kKvqBlock < p.c.ring_state[b] / kKvqBlock - 1))
         s.refused = UA_ERR_INVALID_ARG;
     else if (s.n_new > p.c.cap - s.start)
         s.refused = UA_ERR_CAPACITY;
