@@ -25,7 +25,8 @@ struct SeqState {
 
 // What sequence b appends.  Refused: n_new or start out of range, earlier rows of the start's
 // block not in the ring, capacity.  A call that ends with `end` slots keeps the rows of blocks end/64 - 1 and
-// end/64 (at a border the latter has none yet), so only those of the highest count are sure to be there.
+// end/64 (at a border the latter has none yet).  ring_state says which blocks' rows are there: those from
+// ring_state/64 - 1 on.
 __device__ __forceinline__ SeqState seq_state(const KvqAppendParams& p, int b) {
     SeqState s;
     const int n0 = p.c.n_kept[b];
@@ -328,7 +329,9 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
             if (s.refused) continue;
             const int end = s.start + s.n_new;
             p.c.n_kept[b] = end;
-            p.c.ring_state[b] = s.start == 0 ? end : max(p.c.ring_state[b], end);
+            // from a start on, the rows of its block are the newest whatever was there before (a start inside
+            // the block found its earlier rows there); the block before keeps what was known of it
+            p.c.ring_state[b] = max(end, min(p.c.ring_state[b], (s.start / kKvqBlock + 1) * kKvqBlock));
         }
         if (tid == 0) p.c.ring_state[p.c.B] = 0;
     }

@@ -1,10 +1,12 @@
 """GPU tests of the 8-bit cache's append with tokens taken back: which starts it accepts, and that every start
 it accepts leaves the cache that never saw the tokens taken back."""
+import random
+
 import pytest
 import torch
 
 from kv_cache_compression_ua_b200 import ua
-from softmax_layers import BLOCK, RING, normal
+from softmax_layers import BLOCK, RING, d64, encode, normal, rows_of
 from test_gpu_kvq_cache import check, i32, make, same_bits
 
 pytestmark = pytest.mark.gpu
@@ -24,6 +26,19 @@ def rows(n, seed, B=1, Hkv=1, d=64):
 def put(c, k, v, lo, hi, **kw):
     """Tokens lo .. hi - 1 of k and v, appended in one call."""
     ua.kvq_append(c, k[:, lo:hi].contiguous(), v[:, lo:hi].contiguous(), theta=0.0, **kw)
+
+
+def check_read(c, K, V, n):
+    """What the attention reads of n[b] slots, one KV head: the finished blocks' codes and the unfinished block's rows.  (The
+    block before has its rows in the ring only where the sequence was not taken back behind it.)"""
+    assert c.n_kept.tolist() == n and int(c.ring_state[-1]) == 0
+    for b in range(c.B):
+        for name, X in (("k", K), ("v", V)):
+            got, done = rows_of(c, name, b, 0, n[b]), n[b] // BLOCK * BLOCK
+            for j in range(0, done, BLOCK):
+                codes, s = encode(X[b, j:j + BLOCK, 0], c.k.dtype)
+                assert torch.equal(got[j:j + BLOCK], d64(codes.view(c.k.dtype)) * d64(s)), (name, b, j)
+            assert torch.equal(got[done:], d64(X[b, done:n[b], 0])), (name, b)
 
 
 # a call keeps the rows of the block its end lies in and of the one before: at a border the former has none yet
@@ -97,3 +112,73 @@ def test_every_start_after_every_end(single):
             right = (ring[:, 0, at % RING] == x[:, at, 0]).flatten(1).all(1)
             assert right[taken].all(), (s, end[taken & ~right].tolist())
         assert ua.get_device_status() == (0 if taken.all() else 1)
+
+
+@pytest.mark.parametrize("n", [300, 320, 1000])
+@pytest.mark.parametrize("start", [64, 128, 192])
+@pytest.mark.parametrize("m", [0, 1, 10, 64, 100])
+def test_a_sequence_goes_on_after_a_border_far_back(n, start, m):
+    """A prefix of whole blocks kept, a few tokens appended, then one token at a time past two borders: the cache that
+    never held what was taken back.  The block before the prefix's end has left the ring and is refused."""
+    c = make(1, 1, 64, 1024, E4, BF)
+    k, v = rows(n, 11)
+    k2, v2 = rows(300, 13)
+    put(c, k, v, 0, n)
+    put(c, k2, v2, 0, max(m, 1), start=i32([start]), n_new=i32([m]))
+    for t in range(m, m + 130):
+        put(c, k2, v2, t, t + 1)
+        if t == m:
+            put(c, k2, v2, 0, 1, start=i32([start - 10]))
+            assert ua.get_device_status() == 1
+    assert ua.get_device_status() == 0
+    check(c, *(torch.cat([x[:, :start], y[:, :m + 130]], 1) for x, y in ((k, k2), (v, v2))), [start + m + 130], True)
+
+
+def test_random_walks_of_appends_and_starts():
+    """32 sequences append 0 to 150 tokens at a time, going on, back a little, back to borders and to anywhere.  A model
+    keeps what each row of the ring was last given: an accepted start finds its block's rows there; going on, a border, and
+    up to 64 slots back (not behind the place of the last way back) are never refused; the cache at the end holds the tokens
+    that were kept."""
+    B, T, cap, steps = 32, 150, 704, 60
+    rng = random.Random(5)
+    c = make(B, 1, 64, cap, E4, BF, page=128)
+    K, V = rows(steps * T, 17, B)
+    held = [[] for _ in range(B)]                    # the token in each slot
+    ring = [[None] * RING for _ in range(B)]         # (slot, token)
+    back = [0] * B
+    refused = 0
+    for step in range(steps):
+        start, new = [], []
+        for b in range(B):
+            n = len(held[b])
+            at = rng.choice([n, n, n, max(0, n - rng.randint(1, 64)), BLOCK * rng.randint(0, n // BLOCK), rng.randint(0, n)])
+            m = rng.choice([0, 1, 1, 4, 63, 64, 128, rng.randint(0, T)])
+            m = min(m, T, cap - at)
+            if at + m == n and m:                    # (a refusal leaves n slots too)
+                m -= 1
+            start.append(at)
+            new.append(m)
+        lo = step * T
+        put(c, K, V, lo, lo + T, start=i32(start), n_new=i32(new))
+        got = c.n_kept.tolist()
+        for b, (at, m) in enumerate(zip(start, new)):
+            n, block = len(held[b]), at // BLOCK * BLOCK
+            intact = all(ring[b][j % RING] == (j, held[b][j]) for j in range(block, at))
+            must = at == n or at % BLOCK == 0 or at >= max(n - BLOCK, back[b])
+            assert intact or not must                # (the model itself)
+            if got[b] != at + m:
+                assert got[b] == n and not must, (step, b, n, at, m)
+                refused += 1
+                continue
+            assert intact, (step, b, n, at, m)
+            if at < n:
+                back[b] = at
+            held[b] = held[b][:at] + list(range(lo, lo + m))
+            for j in range(max(at, ((at + m) // BLOCK - 1) * BLOCK), at + m):
+                ring[b][j % RING] = (j, held[b][j])
+        assert ua.get_device_status() in (0, 1)
+    assert 0 < refused < B * steps // 4
+    n = [len(x) for x in held]
+    idx = torch.tensor([x + [0] * (cap - len(x)) for x in held], device="cuda")
+    pick = torch.arange(B, device="cuda")[:, None]
+    check_read(c, K[pick, idx], V[pick, idx], n)
