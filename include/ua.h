@@ -423,7 +423,8 @@ ua_status ua_qk_norm_rope_bwd(const ua_qk_shape* shape, const void* q, const voi
  * access is skipped.  capacity < 2^30.
  * A key or value that is not finite makes its whole block's scale NaN when the block is encoded:
  * every output row that sees a slot of that block is then NaN, and no other.  Codes are always
- * finite (a cache filled by other means must hold finite codes too). */
+ * finite (a cache filled by other means must hold finite codes too).  In the unfinished block it spoils the output
+ * rows that see its own slot, a value in its element only, and no other row. */
 typedef enum { UA_KVQ_INT8 = 0, UA_KVQ_E4M3 = 1 } ua_kvq_format;
 
 typedef struct {

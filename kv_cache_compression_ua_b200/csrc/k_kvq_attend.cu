@@ -256,10 +256,13 @@ template <int DH, int NT> __device__ __forceinline__ void init_state(State<DH, N
 // in the warp's ring (kt, vt: [16][DH]; rows at and behind n are not there): bf16 products, the operands
 // as sums of bf16 parts (bf16 activations are one part, fp32 ones three; pairs of parts below 2^-24 of
 // the product are left out).
+// A row past its own slot has probability 0 there, and 0 times a value that is not finite is NaN: where some row ends
+// within these tokens (drafts; lim_min: the least of the rows' last slots), such values are left out of the
+// products and added to the rows that see them (as bf16 parts: values above bf16's largest, too).
 template <typename T, int DH, int NT, bool E4M3>
 __device__ __forceinline__ void tail_part(const KvqAttendParams& p, typename Att<T, DH, NT, E4M3>::Smem& sm,
                                           State<DH, NT>& st, const T* kt, const T* vt, const float* bias, int slot0,
-                                          int n) {
+                                          int n, int lim_min) {
     using A = Att<T, DH, NT, E4M3>;
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     bool hidden[2];                                      // tokens no row sees: their rows may be anything
@@ -325,6 +328,8 @@ __device__ __forceinline__ void tail_part(const KvqAttendParams& p, typename Att
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) st.l[nt][e] = fmaf(st.l[nt][e], corr[nt][e], x[0][nt][e] + x[0][nt][e + 2]);
+    const bool drafts = min(n, slot0 + 16) - 1 > lim_min;
+    auto held = [](float v) { return fabsf(v) <= 3.3895314e38f; };      // as sums of bf16 parts
     uint2 pb[A::TPP][NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -347,6 +352,18 @@ __device__ __forceinline__ void tail_part(const KvqAttendParams& p, typename Att
                 Vec16<T>::ld(src, v[i]);
                 if constexpr (A::F32) Vec16<T>::ld(src + 4, v[i] + 4);
             }
+        }
+        bool left_out = false;
+        if (drafts) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (!held(v[i][e])) {
+                        v[i][e] = 0.f;
+                        left_out = true;
+                    }
+            left_out = __any_sync(0xffffffffu, left_out);
         }
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
@@ -372,6 +389,24 @@ __device__ __forceinline__ void tail_part(const KvqAttendParams& p, typename Att
                 for (int e = 0; e < 4; ++e)
                     st.o[4 * pass + mt][nt][e] =
                         fmaf(st.o[4 * pass + mt][nt][e], corr[nt][e & 1], any[nt][e & 1] ? acc[nt][e] : 0.f);
+            }
+        }
+        if (left_out) {
+#pragma unroll 1
+            for (int t = 0; t < 16; ++t) {
+                if (((t < 8 ? hid[0] : hid[1]) >> (4 * (2 * (t & 3) + ((t >> 2) & 1)))) & 1u) continue;
+                float w[8];
+                Vec16<T>::ld(vt + t * DH + 64 * pass + 8 * r, w);
+                if constexpr (A::F32) Vec16<T>::ld(vt + t * DH + 64 * pass + 8 * r + 4, w + 4);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const bool sees = slot0 + t <= sm.lim[8 * nt + 2 * c + (e & 1)];
+#pragma unroll
+                        for (int mt = 0; mt < 4; ++mt)
+                            if (sees && !held(w[2 * mt + (e >> 1)])) st.o[4 * pass + mt][nt][e] += 2.f * w[2 * mt + (e >> 1)];
+                    }
             }
         }
     }
@@ -501,7 +536,7 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
                     const unsigned char* at = sm.ring[warp] + stg * 2 * A::KB;
                     tail_part<T, DH, NT, E4M3>(p, sm, st, reinterpret_cast<const T*>(at),
                                                reinterpret_cast<const T*>(at + A::KB),
-                                               bias0 ? sm.bias[warp][stg] : nullptr, slot0, n);
+                                               bias0 ? sm.bias[warp][stg] : nullptr, slot0, n, lim_min);
                 }
                 load_k(next, i + A::NSTG, stg);          // (no page: left out)
                 load_v(next, stg);
