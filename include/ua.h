@@ -382,7 +382,8 @@ typedef struct {
  *   y = R(pos) n   (pairs m, m + d/2, angle pos * theta^(-2m/d); rope_theta == 0: y = n)
  * q, q_out [B,T,H,d] act; k, k_out [B,T,Hkv,d] act; wq, wk [d] f32 or NULL; pos [B,T] int32 or
  * NULL (pos = t).  Either q and q_out or k and k_out may both be NULL (that side is left out).
- * Sums, angles (double) and the rotation are held in 32 bits or more; one rounding at the end. */
+ * Sums, angles (double) and the rotation are held in 32 bits or more; one rounding at the end.  The
+ * squares are summed in fp32: with a gain, elements up to 2^60 in magnitude. */
 ua_status ua_qk_norm_rope_fwd(const ua_qk_shape* shape, const void* q, const void* k, const float* wq,
                               const float* wk, const int32_t* pos, void* q_out, void* k_out, void* stream);
 
@@ -423,7 +424,7 @@ ua_status ua_qk_norm_rope_bwd(const ua_qk_shape* shape, const void* q, const voi
  * access is skipped.  capacity < 2^30.
  * A key or value that is not finite makes its whole block's scale NaN when the block is encoded:
  * every output row that sees a slot of that block is then NaN, and no other.  Codes are always
- * finite (a cache filled by other means must hold finite codes too).  In the unfinished block it spoils the output
+ * finite, scales zero, positive or NaN (a cache filled by other means must hold such ones too).  In the unfinished block it spoils the output
  * rows that see its own slot, a value in its element only, and no other row. */
 typedef enum { UA_KVQ_INT8 = 0, UA_KVQ_E4M3 = 1 } ua_kvq_format;
 
@@ -469,6 +470,8 @@ ua_status ua_kvq_append(const ua_kvq* cache, const ua_qk_shape* shape, const voi
  * log-biases or FoX's forget gate; any finite value, the lowest too, only weighs).  g [B,Tq,H,d]
  * act or NULL (no gate).  o [B,Tq,H,d] act; lse [B,H,Tq] f32 natural log or NULL.  A query that
  * sees nothing gets o = 0, lse = -inf; rows i >= n_q[b] of o and lse are left as they were.
+ * Logits are formed in fp32 and have to fit there; weighted values are summed there with weights of up to 2^14:
+ * values up to 2^80 in magnitude.
  * Any Tq >= 1; made for single tokens and drafts (16 rows Tq*H/Hkv per pass over the cache).
  * n_kept outside [0, capacity] or n_q outside [0, Tq] raises UA_ERR_INVALID_ARG in the device
  * status and the sequence is taken as empty.  ws: zeroed once before its first use (and again after
