@@ -416,7 +416,8 @@ ua_status ua_qk_norm_rope_bwd(const ua_qk_shape* shape, const void* q, const voi
  *   k_ring, v_ring  [B, Hkv, 128, d] act
  *   n_kept [B] int32 slots filled;  ring_state [B+1] int32: per sequence a slot count r that says
  *   which rows the ring holds, those of the filled slots from block floor(r/64) - 1 on, then a counter of the
- *   append that is zero between calls (initialise: the values of n_kept, then 0)
+ *   append that is zero between calls (initialise: the values of n_kept, or 0 where codes came from elsewhere
+ *   and the ring is empty, n_kept on a block's border; then 0)
  * page_table == NULL: one page of `capacity` slots per sequence (page b; capacity a multiple of
  * 64).  Otherwise slot j of sequence b lies in page page_table[b*max_pages + j/page_size], page_size a
  * power of two, 128 <= page_size <= 2^20, capacity == max_pages*page_size.  Page ids are checked
@@ -453,8 +454,9 @@ typedef struct {
  * start below n_kept takes tokens back (rejected drafts, or a shared prefix of whole blocks): it must lie
  * on a block's first slot, or its block's earlier rows must be in the ring: floor(start/64) >=
  * floor(ring_state[b]/64) - 1, and start <= ring_state[b].  Always so for up to 64 tokens taken back, not further
- * than to where a sequence was last taken back.  ring_state[b] becomes max(start + n_new, min(ring_state[b],
- * 64*floor(start/64) + 64)), so a sequence goes on from wherever it was taken back to.
+ * than to where a sequence was last taken back.  With e = 64*floor(start/64) + 64, ring_state[b] becomes max(start +
+ * n_new, min(ring_state[b], e)), or max(start + n_new, e) from a value below start: a sequence goes on from wherever it
+ * was taken back to.
  * A start above n_kept, below 0 or without its rows, or n_new outside [0, T], raises UA_ERR_INVALID_ARG in
  * the device status, a sequence that would pass the capacity UA_ERR_CAPACITY; that sequence is left as it
  * was.  Calls on one cache must not overlap on the GPU. */

@@ -330,8 +330,10 @@ __global__ void __launch_bounds__(4 * DH, DH == 64 ? 3 : 1) k_kvq_append(KvqAppe
             const int end = s.start + s.n_new;
             p.c.n_kept[b] = end;
             // from a start on, the rows of its block are the newest whatever was there before (a start inside
-            // the block found its earlier rows there); the block before keeps what was known of it
-            p.c.ring_state[b] = max(end, min(p.c.ring_state[b], (s.start / kKvqBlock + 1) * kKvqBlock));
+            // the block found its earlier rows there); the block before keeps what was known of it (nothing, where
+            // the count was set by hand to a border: ring_state below the start)
+            const int border = (s.start / kKvqBlock + 1) * kKvqBlock, was = p.c.ring_state[b];
+            p.c.ring_state[b] = max(end, was < s.start ? border : min(was, border));
         }
         if (tid == 0) p.c.ring_state[p.c.B] = 0;
     }

@@ -182,3 +182,23 @@ def test_random_walks_of_appends_and_starts():
     idx = torch.tensor([x + [0] * (cap - len(x)) for x in held], device="cuda")
     pick = torch.arange(B, device="cuda")[:, None]
     check_read(c, K[pick, idx], V[pick, idx], n)
+
+
+@pytest.mark.parametrize("m", [1, 10, 64, 70])
+def test_a_prefix_without_rows_is_not_taken_for_one(m):
+    """A slot count set by hand on a block's border (codes from elsewhere, nothing in the ring): the sequence goes on from
+    it, and a start inside the prefix's last block stays refused however it goes on."""
+    c = make(1, 1, 64, 512, E4, BF)
+    k, v = rows(400, 21)
+    c.n_kept.fill_(128)
+    put(c, k, v, 0, m)
+    assert c.n_kept.tolist() == [128 + m] and ua.get_device_status() == 0
+    for n_new in (0, 1):
+        put(c, k, v, 0, 1, start=i32([100]), n_new=i32([n_new]))
+        assert ua.get_device_status() == 1 and c.n_kept.tolist() == [128 + m]
+    put(c, k, v, m, m + 1)
+    put(c, k, v, m, m + 1, start=i32([128 + m]))     # one token back
+    put(c, k, v, m + 1, m + 100)
+    assert ua.get_device_status() == 0
+    n, lead = 128 + m + 100, torch.zeros_like(k[:, :128])
+    check_read(c, torch.cat([lead, k], 1), torch.cat([lead, v], 1), [n])
