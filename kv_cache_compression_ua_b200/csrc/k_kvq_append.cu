@@ -9,8 +9,9 @@
 // write of its code, so the block's largest magnitude costs one reduction and no second read.  A
 // token's gain and rotation are one set of coefficients for all hpc heads; the next head's rows are
 // copied meanwhile (a thread's own queue).  32 x 4096 tokens, 8 heads of 64, bf16 to e4m3: 83 us,
-// 4.8 TB/s; issue slots bind (its share of a prompt with 32 query heads: half, 8 x 4096 tokens 63 us
-// together, 84 % of the copy bandwidth).  The step of 32 tokens: 5.2 us.
+// 4.9 TB/s; issue slots bind (its share of a prompt with 32 query heads: 28 of 68 us for 8 x 4096 tokens).  8 x 4096
+// tokens with queries to int8: 73 us; fp32 to e4m3 122, to int8 134.  The step of 32 tokens: 4.5 us.
+// At DH = 64 three CTAs an SM leave 80 registers a thread: fp32 to int8 spills 180 bytes, to e4m3 28, bf16 to int8 48.
 #include "qk_norm.cuh"
 #include "ua_profile.h"
 

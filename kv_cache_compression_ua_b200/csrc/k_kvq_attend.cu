@@ -19,18 +19,21 @@
 //   * a logit is one fused multiply-add and an exp2 from the product where nothing is masked.
 // Queries enter as f16 scaled by a power of two for each row (bf16 queries exactly; fp32 ones as a high
 // and a low part), probabilities as f16 times 2^14 (fp32: high and low part), so that small
-// probabilities of long caches keep 2^-38 of the row's maximum; sums and statistics are fp32.
+// probabilities of long caches keep 2^-38 of the row's maximum; sums and statistics are fp32.  One f16 part rounds a
+// probability by 2^-11 of it at most, an eighth of the half step of 2^-8 by which a bf16 output is rounded anyway
+// (outputs are off by 1.7e-3 against 64 bits, as with fp32 probabilities), and a second part would double the second
+// product; int8's offset of 128 costs two bits of the fp32 sums, far below that.
 //
 // Split, by lengths read on the device: few units (sequence, KV head, row tile) get whole CTAs each;
 // otherwise the blocks of all units are laid out flat, with kUnitCost more for each unit, and cut into equal runs,
 // one a CTA.  A unit in several CTAs is merged by the last of them to arrive, in the order of the blocks:
 // the result does not depend on who that is.
 //
-// Measured: 32 sequences of about 16k slots, 8 heads of 64, int8 (448 MB): 80 us, 5.6 TB/s (86 % of the copy bandwidth;
-// the copies alone 74 us; what is left is the ALU pipe, 2 clocks a warp instruction); one of
+// Measured (in a captured graph): 32 sequences of about 16k slots, 8 heads of 64, int8 (448 MB): 80 us, 5.6 TB/s (85 % of
+// the copy bandwidth; the copies alone 74 us; what is left is the ALU pipe, 2 clocks a warp instruction); one of
 // 262144 slots, 8 heads of 128, e4m3 (537 MB): 93 us, 5.8 TB/s (88 %; the copies alone 85 us, SMs of the
 // larger clusters finish last); 4 of about 8192 with bias and gate (57 MB): 22 us, of it 7 us before the
-// first products and 5 us of merging; one of 333 slots: 7.4 us.
+// first products and 5 us of merging; one of 333 slots: 6.9 us.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -177,8 +180,11 @@ template <typename T, int DH, int NT, bool E4M3> struct Att {
     static constexpr int KB = 64 * DH;               // bytes of a block's keys
     static constexpr int QS = DH + 4;                // row stride of the queries in shared memory
     static constexpr int NM = DH / 16;               // 16-element tiles of the output
-    // One CTA an SM, of as many warps as its registers allow (168 or 255 a thread): few CTAs make few
-    // parts to merge.
+    // One CTA an SM, of as many warps as its registers allow (128, 168 or 255 a thread): few CTAs make few
+    // parts to merge.  The forms of one row tile spill 86 to 202 bytes a thread at that (bf16: 86 and 182 at DH = 64,
+    // 182 and 190 at 128), those of two 150 to 278 at DH = 128 (at 64 up to 34, fp32 only).  With 12 (DH = 64) and 8 warps the bf16 forms of one tile
+    // spill nothing, and four bf16 cases measured faster (1B decode step 80.4 -> 77.9 us, the long sequence 93.1 ->
+    // 84.9); fp32 has not been measured so.
     static constexpr int kWarps = NT == 1 ? (DH == 64 ? 16 : 12) : 8, kThreads = 32 * kWarps;
     static constexpr int kBufs = kWarps / 4;         // buffers the warps' O are added up in
     static constexpr int kMinItems = kWarps + kUnitCost;    // fewest items (blocks and unit costs) of a run
@@ -676,10 +682,9 @@ template <typename T, int DH, int NT, bool E4M3> struct Walk {
                     pb[1][mt][nt] = make_uint2(transpose8x8(pack_f16(x[mt][nt][0] - l2.x, x[mt][nt][1] - l2.y)),
                                                transpose8x8(pack_f16(x[mt][nt][2] - h2.x, x[mt][nt][3] - h2.y)));
                 }
-                if constexpr (A::OFF) {
+                if constexpr (A::OFF) {                  // (bf16: one part)
                     if (mt == 0) mma_f16(sum[nt], ones, pb[0][mt][nt], none);
                     else mma_f16(sum[nt], ones, pb[0][mt][nt]);
-                    if constexpr (A::PP == 2) mma_f16(sum[nt], ones, pb[1][mt][nt]);
                 }
             }
         bool rescale = false;

@@ -8,8 +8,8 @@
 //   * few instructions an element, for at 6.5 TB/s an SM has some 280 issue slots a warp for 3 KB: packed
 //     fp32 arithmetic, a token's angles once for all its heads (90 -> 83 us; copy bandwidth: 82);
 //   * the backward's angles a thread's own, without barriers, from positions fetched a tile ahead: 169 ->
-//     140 us (123), 88 % of the copy bandwidth; what is left is issue slots (58 % busy at 16 warps an SM,
-//     128 registers a thread).
+//     139 us (123), 88 % of the copy bandwidth; what is left is issue slots (60 % busy at 16 warps an SM,
+//     128 registers a thread; with the rotation 24 (bf16) or 32 bytes of them spill).
 #include "qk_norm.cuh"
 #include "ua_profile.h"
 
@@ -40,7 +40,8 @@ __global__ void __launch_bounds__(kNth, 3) k_qk_norm_fwd(QkNormParams p) {
 
 // Backward.  The first ctas_q CTAs take the queries, the others the keys (in proportion to their
 // heads), each an equal run of (token tile, four heads) items; the loads of the next items are always on their way (a thread's own queue in shared memory).  It keeps the gain
-// gradient of its lanes' elements in registers (fp32), sums it over its rows in shared memory at the
+// gradient of its lanes' elements in registers (fp32: no chain is longer than a lane's own terms; off by 2.4e-7 of
+// the largest for 270000 tokens of 128 heads), sums it over its rows in shared memory at the
 // end and writes one partial row; k_qk_norm_dw adds the CTAs' rows in a fixed order.
 template <typename T> struct BwdQueue {
     static constexpr int NV = Raw8<T>::NV, DEPTH = 3;
@@ -241,7 +242,7 @@ template <typename T, int DH> cudaError_t fwd(const QkNormParams& p, cudaStream_
     constexpr int TOK = norm_tokens<DH, kNth>(), smem = NormTile<T, DH, kNth>::Queue::kBytes;
     const long long tiles = (p.N + TOK - 1) / TOK;
     // few tokens: the heads are split over CTAs too, while all of them fit the SMs' three places (2 x 777
-    // tokens, 32 + 8 heads of 64: 7.1 us with a CTA an SM, 5.2 with three; in two rounds, 6.2)
+    // tokens, 32 + 8 heads of 64: 6.6 us with a CTA an SM, 4.6 with three; in two rounds, 5.6)
     const int quads = head_quads(p), places = 3 * 148;
     const int split = (int)(tiles >= places ? 1 : (quads < places / tiles ? quads : places / tiles));
     cudaError_t e = cudaFuncSetAttribute(k_qk_norm_fwd<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

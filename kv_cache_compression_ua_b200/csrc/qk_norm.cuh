@@ -134,7 +134,7 @@ template <typename T, int DH> __device__ __forceinline__ void pairs_at(const flo
 // cos / sin of pos * f, given gt = f / (2 pi): the angle in turns is formed in double precision and its
 // nearest integer removed exactly, so far positions keep the accuracy of the sine of the remainder.
 // fp32 results take sincospi (1 to 2 ulp); bf16 ones the fast unit, whose absolute error on
-// [-pi, pi], below 2^-20, is far under their half step of 2^-9 of the pair's size.
+// [-pi, pi], below 2^-20, is far under their half step of 2^-8 of the pair's size.
 template <typename T> __device__ __forceinline__ void rope_cs_turn(int pos, double gt, float* c, float* s) {
     const double a = (double)pos * gt;
     const float r = (float)(a - rint(a));

@@ -1009,13 +1009,13 @@ ua_status ua_kvq_append(const ua_kvq* c, const ua_qk_shape* s, const void* q, co
     p.n_new = n_new; p.start = start;
     p.nb = (int)(((long long)s->T + 2 * kKvqBlock - 2) / kKvqBlock);
     // All KV heads in one CTA share a token's angles; fewer heads a CTA where the blocks alone leave SMs
-    // idle (3B chunk of 4 x 1003 tokens: one head each 30 us, two 22 us).  A step of less than a block
-    // has a row or a few a CTA and is latency: one head each (32 tokens of the 1B shape, cold: 7.3 us, two
-    // heads 9.4 us).
+    // idle (3B chunk of 4 x 1003 tokens: one head each 27.3 us, two 22.2, four 20.4, eight 26.8).  A step of less than a
+    // block has a row or a few a CTA and is latency: one head each (32 tokens of the 1B shape: one to four heads
+    // 4.3 us, eight 5.7).
     // More CTAs also where they cut the rounds that the SMs' places take, each as long as its heads, by a
-    // fifth (1B shape, with queries: 8 x 4096 tokens, 520 CTAs of 8 heads 72.4 us, 1040 of four 68.8; 12 x 4096,
-    // rounds alike, 97.5 and 98.0); below four heads the repeated angles cost as much (4 x 1003 tokens, four
-    // heads 11.9, two 13.7).
+    // fifth (1B shape, with queries: 8 x 4096 tokens, 520 CTAs of 8 heads 72.2 us, 1040 of four 68.2; 12 x 4096,
+    // rounds alike, 97.5 and 98.2); below four heads the repeated angles cost as much (4 x 1003 tokens, four
+    // heads 12.4, two 14.6).
     p.hpc = s->T < kKvqBlock ? 1 : s->Hkv;
     const int places = s->d == 64 ? 3 * 148 : 148;
     auto ctas = [&](int hpc) { return (long long)s->B * p.nb * (s->Hkv / hpc); };
@@ -1028,8 +1028,11 @@ ua_status ua_kvq_append(const ua_kvq* c, const ua_qk_shape* s, const void* q, co
     }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     // The queries of many tokens run in their own kernel beside the blocks' one (smaller CTAs, more of
-    // them an SM); those of a few steps in further CTAs of the same launch, as do queries whose positions
-    // are slot counts that this call changes (given as start or pos, too: those CTAs read them first).
+    // them an SM: 8 x 4096 tokens 67.9 us, in the same launch 73.0; 2400 tokens of the 3B shape 15.4 and 19.1); those of a
+    // few steps in further CTAs of the same launch (32 tokens 4.5 us, apart 5.2; 600 5.7 and 6.3), as do
+    // queries whose positions are slot counts that this call changes (given as start or pos, too: those CTAs
+    // read them first).  Between 1000 tokens and the 2368 of the rule, apart is often the faster one
+    // already (2000 tokens of the 1B shape 8.1 us, in the same launch 10.0; of the 3B shape 14.2 and 14.0).
     const bool apart = q && p.n.N >= 148 * 16 &&
                        (!p.n.rope || (pos ? pos != c->n_kept : start != nullptr && start != c->n_kept));
     if (q && !apart) {

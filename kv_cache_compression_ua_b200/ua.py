@@ -766,8 +766,9 @@ KVQ_FORMATS = {torch.int8: UA_KVQ_INT8, torch.float8_e4m3fn: UA_KVQ_E4M3}
 class KVQCache:
     """Device tensors of one 8-bit cache of a softmax layer (see ua_kvq in ua.h).  k, v: codes [pages, Hkv,
     page_size, d] (torch.int8 or torch.float8_e4m3fn), k_scale, v_scale [pages, Hkv, page_size/64],
-    k_ring, v_ring [B, Hkv, 128, d] in the activation type `dtype`, n_kept [B].  Without a page_table [B, max_pages]
-    sequence b is page b.  The tensors are checked once, here, and must stay the ones given."""
+    k_ring, v_ring [B, Hkv, 128, d] in the activation type `dtype`, n_kept [B], ring_state [B + 1] (which rows the ring
+    holds; None: those up to n_kept).  Without a page_table [B, max_pages] sequence b is page b.  The tensors are
+    checked once, here, and must stay the ones given."""
     B: int
     Hkv: int
     d: int
@@ -858,8 +859,9 @@ class KVQCache:
 def kvq_append(cache: KVQCache, k, v, q=None, *, wq=None, wk=None, pos=None, n_new=None, start=None, eps=1e-6,
                theta=500000.0, q_out=None, stream=None):
     """ua_kvq_append: append k, v [B,T,Hkv,d] (the first n_new[b] tokens of sequence b), the keys
-    normalised (wk) and rotated on the way; start [B] int32 takes tokens back first.  With q [B,T,H,d]
-    the queries are normalised (wq) and rotated in the same launch and returned."""
+    normalised (wk) and rotated on the way; start [B] int32 takes tokens back first: to any block's first
+    slot, or inside the last blocks, up to 64 slots always.  With q [B,T,H,d] the queries are normalised (wq) and
+    rotated in the same call and returned."""
     if stream is not None:
         return _on_stream(stream, cache, kvq_append, cache, k, v, q, wq=wq, wk=wk, pos=pos, n_new=n_new, start=start,
                           eps=eps, theta=theta, q_out=q_out)
@@ -899,8 +901,8 @@ def kvq_attend(cache: KVQCache, q, *, g=None, bias=None, n_q=None, scale=None, o
                stream=None):
     """ua_kvq_attend: attention of the last queries q [B,H,d] or [B,Tq,H,d] (the first n_q[b] of
     them) over the cache.  bias [B,Hkv,capacity] f32 is added to the logits, g (like q) gates the output, lse
-    [B,H,Tq] f32 receives the row normalisers.  ws: kvq_attend_workspace_size bytes, zeroed once (a fresh
-    one is made without it).  Returns o, shaped like q."""
+    [B,H,Tq] f32 receives the row normalisers.  ws: kvq_attend_workspace_size bytes, zeroed once (without it
+    a fresh one, some 2.5 MB, is made and zeroed in every call).  Returns o, shaped like q."""
     if stream is not None:
         return _on_stream(stream, cache, kvq_attend, cache, q, g=g, bias=bias, n_q=n_q, scale=scale, out=out, lse=lse, ws=ws)
     if q.dim() not in (3, 4):
