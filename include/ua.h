@@ -424,9 +424,9 @@ ua_status ua_qk_norm_rope_bwd(const ua_qk_shape* shape, const void* q, const voi
  * where they are used: one outside [0, pool_pages) raises UA_ERR_INVALID_ARG in the device status and its
  * access is skipped.  capacity < 2^30.
  * A key or value that is not finite makes its whole block's scale NaN when the block is encoded:
- * every output row that sees a slot of that block is then NaN, and no other.  Codes are always
- * finite, scales zero, positive or NaN (a cache filled by other means must hold such ones too).  In the unfinished block it spoils the output
- * rows that see its own slot, a value in its element only, and no other row. */
+ * every output row that sees a slot of that block is then NaN, and no other.  In the unfinished block it
+ * spoils the output rows that see its own slot, a value in its element only, and no other row.  Codes are
+ * always finite, scales zero, positive or NaN (a cache filled by other means must hold such ones too). */
 typedef enum { UA_KVQ_INT8 = 0, UA_KVQ_E4M3 = 1 } ua_kvq_format;
 
 typedef struct {
@@ -453,10 +453,10 @@ typedef struct {
  * single token's pos, may be n_kept itself.
  * start below n_kept takes tokens back (rejected drafts, or a shared prefix of whole blocks): it must lie
  * on a block's first slot, or its block's earlier rows must be in the ring: floor(start/64) >=
- * floor(ring_state[b]/64) - 1, and start <= ring_state[b].  Always so for up to 64 tokens taken back, not further
- * than to where a sequence was last taken back.  With e = 64*floor(start/64) + 64, ring_state[b] becomes max(start +
- * n_new, min(ring_state[b], e)), or max(start + n_new, e) from a value below start: a sequence goes on from wherever it
- * was taken back to.
+ * floor(ring_state[b]/64) - 1, and start <= ring_state[b].  Always so for up to 64 tokens taken back, but not
+ * further than to where the sequence was last taken back, nor into a prefix whose rows the ring never held.
+ * With e = 64*floor(start/64) + 64, ring_state[b] becomes max(start + n_new, min(ring_state[b], e)), or
+ * max(start + n_new, e) from a value below start: a sequence goes on from wherever it was taken back to.
  * A start above n_kept, below 0 or without its rows, or n_new outside [0, T], raises UA_ERR_INVALID_ARG in
  * the device status, a sequence that would pass the capacity UA_ERR_CAPACITY; that sequence is left as it
  * was.  Calls on one cache must not overlap on the GPU. */

@@ -182,9 +182,9 @@ template <typename T, int DH, int NT, bool E4M3> struct Att {
     static constexpr int NM = DH / 16;               // 16-element tiles of the output
     // One CTA an SM, of as many warps as its registers allow (128, 168 or 255 a thread): few CTAs make few
     // parts to merge.  The forms of one row tile spill 86 to 202 bytes a thread at that (bf16: 86 and 182 at DH = 64,
-    // 182 and 190 at 128), those of two 150 to 278 at DH = 128 (at 64 up to 34, fp32 only).  With 12 (DH = 64) and 8 warps the bf16 forms of one tile
-    // spill nothing, and four bf16 cases measured faster (1B decode step 80.4 -> 77.9 us, the long sequence 93.1 ->
-    // 84.9); fp32 has not been measured so.
+    // 182 and 190 at 128), those of two 150 to 278 at DH = 128 (at 64 up to 34, fp32 only).  With 12 (DH = 64) and 8
+    // warps the bf16 forms of one tile spill nothing, and four bf16 cases measured faster (1B decode step 80.4 ->
+    // 77.9 us, the long sequence 93.1 -> 84.9); fp32 has not been measured so.
     static constexpr int kWarps = NT == 1 ? (DH == 64 ? 16 : 12) : 8, kThreads = 32 * kWarps;
     static constexpr int kBufs = kWarps / 4;         // buffers the warps' O are added up in
     static constexpr int kMinItems = kWarps + kUnitCost;    // fewest items (blocks and unit costs) of a run

@@ -860,8 +860,8 @@ def kvq_append(cache: KVQCache, k, v, q=None, *, wq=None, wk=None, pos=None, n_n
                theta=500000.0, q_out=None, stream=None):
     """ua_kvq_append: append k, v [B,T,Hkv,d] (the first n_new[b] tokens of sequence b), the keys
     normalised (wk) and rotated on the way; start [B] int32 takes tokens back first: to any block's first
-    slot, or inside the last blocks, up to 64 slots always.  With q [B,T,H,d] the queries are normalised (wq) and
-    rotated in the same call and returned."""
+    slot, or up to 64 of the tokens since they were last taken back.  With q [B,T,H,d] the queries are normalised (wq)
+    and rotated in the same call and returned."""
     if stream is not None:
         return _on_stream(stream, cache, kvq_append, cache, k, v, q, wq=wq, wk=wk, pos=pos, n_new=n_new, start=start,
                           eps=eps, theta=theta, q_out=q_out)
